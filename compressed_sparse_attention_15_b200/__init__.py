@@ -9,10 +9,15 @@ library is loaded on first use and its absence is an error.
 from . import ops, step, synth, workloads  # noqa: F401
 from .ops import (  # noqa: F401
     Workspace,
+    add_rmsnorm,
     compress,
     hca_mqa,
     index_scores,
     index_topk,
+    paged_append,
+    paged_hca_mqa,
+    paged_read,
+    paged_sparse_mqa,
     sparse_mqa,
     topk,
     num_entries,

@@ -15,6 +15,7 @@ CSA_OK = 0
 CSA_DTYPE_F32 = 0
 CSA_DTYPE_BF16 = 1
 CSA_DTYPE_E4M3 = 2
+CSA_CACHE_INT4 = 3
 CSA_MAX_TOPK = 2048
 CSA_STEP_CHAINED = 0
 CSA_STEP_PERSISTENT = 1
@@ -32,6 +33,7 @@ SIGNATURES = {
                                _P]),
     "csa_index_compress": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _LL, _LL, _LL, _I, _I, _P]),
     "csa_hadamard_rows": (_I, [_P, _P, _P, _LL, _I, _I, _I, _P]),
+    "csa_add_rmsnorm": (_I, [_P, _LL, _P, _P, _F, _P, _P, _P, _LL, _I, _I, _I, _I, _P]),
     "csa_index_topk_workspace_bytes": (_SZ, [_I, _I, _I]),
     "csa_index_topk": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
     "csa_index_scores": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
@@ -45,6 +47,14 @@ SIGNATURES = {
     "csa_topk_sparse_mqa_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "csa_topk_sparse_mqa": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _F, _P, _I, _I, _I, _I, _I, _I, _P, _I, _I, _I, _P,
                                  _SZ, _P]),
+    "csa_paged_append": (_I, [_P, _LL, _LL, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_double, _P, _I, _I,
+                              _I, _P, _SZ, _P]),
+    "csa_paged_read": (_I, [_P, _P, _P, _P, _P, _P, _LL, _I, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "csa_paged_mqa_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "csa_paged_sparse_mqa": (_I, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _I, _I,
+                                  _I, _P, _SZ, _P]),
+    "csa_paged_hca_mqa": (_I, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P,
+                               _SZ, _P]),
     "csa_workspace_status": (_I, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "csa_launch_count": (ctypes.c_ulonglong, []),
     "csa_index_topk_noalloc": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P]),

@@ -152,6 +152,27 @@ int csa_hadamard_rows(const void *x, void *out, float *out_scales, long long row
                                       fp8 ? out_scales : nullptr, rows, D, dtype, (cudaStream_t)stream));
 }
 
+int csa_add_rmsnorm(const void *x, long long x_stride, const void *residual, const float *weight, float eps, void *out,
+                    float *out_scales, void *sum_out, long long rows, int D, int group, int dtype, int out_dtype,
+                    csa_stream_t stream) {
+  if (!dtype_ok(dtype) || rows < 0 || D < 1 || D > 16384 || !(eps >= 0.f)) return CSA_ERR_INVALID;
+  if (x_stride == 0) x_stride = D;
+  if (x_stride < D) return CSA_ERR_INVALID;
+  const bool fp8 = out_dtype == CSA_DTYPE_E4M3;
+  if (!fp8 && (out_dtype != dtype || group != 0)) return CSA_ERR_INVALID;
+  if (group != 0 && ((group != 32 && group != 64 && group != 128 && group != 256) || D % group)) return CSA_ERR_INVALID;
+  if (rows == 0) return CSA_OK;
+  if (!x || !weight || !out || (residual != nullptr) != (sum_out != nullptr)) return CSA_ERR_INVALID;
+  if (fp8 && (!out_scales || (reinterpret_cast<uintptr_t>(out_scales) & 3))) return CSA_ERR_INVALID;
+  if (!elem_aligned(x, dtype) || !elem_aligned(residual, dtype) || !elem_aligned(sum_out, dtype) ||
+      (!fp8 && !elem_aligned(out, dtype)) || (reinterpret_cast<uintptr_t>(weight) & 3))
+    return CSA_ERR_INVALID;
+  if (!device_ok()) return CSA_ERR_UNSUPPORTED;
+  NormArgs a{x,    residual, weight, out, sum_out, fp8 ? out_scales : nullptr, rows, x_stride, D, group ? group : D,
+             dtype, eps};
+  return cuda_rc(launch_add_rmsnorm(a, (cudaStream_t)stream));
+}
+
 size_t csa_topk_workspace_bytes(int Q, int N_max, int k) {
   if (Q < 1 || N_max < 1 || k < 1) return kStatusBytes;
   return kStatusBytes + align256(topk_scratch_bytes(Q, N_max, k));
@@ -372,6 +393,149 @@ int csa_topk_sparse_mqa(const float *scores, const int32_t *n_cmp, int k, int32_
   a.scores = nullptr;
   a.idx_out = nullptr;
   return cuda_rc(launch_mqa(a, (cudaStream_t)stream));
+}
+
+// The page cache's arguments; fills c. rows: the entry points that move rows
+// (D up to 4096); attention takes D up to 1024.
+static int check_cache(const void *pages, const uint8_t *scales, const int32_t *page_table, int num_pages,
+                       int page_size, int pages_per_seq, int D, int max_D, int dtype, int cache_dtype,
+                       PagedCache *c) {
+  if (!pages || (reinterpret_cast<uintptr_t>(page_table) & 3)) return CSA_ERR_INVALID;
+  if (!dtype_ok(dtype) || num_pages < 1 || page_size < 1 || pages_per_seq < 1 || D < 1 || D > max_D)
+    return CSA_ERR_INVALID;
+  if ((long long)pages_per_seq * page_size > 0x7fffffffLL - (1 << 20)) return CSA_ERR_INVALID;
+  const bool int4 = cache_dtype == CSA_CACHE_INT4;
+  if (int4 ? (!scales || D % 16 || (reinterpret_cast<uintptr_t>(pages) & 7))
+           : (scales || cache_dtype != dtype || !elem_aligned(pages, dtype)))
+    return CSA_ERR_INVALID;
+  *c = PagedCache{static_cast<const uint8_t *>(pages), scales, page_table, num_pages, page_size, pages_per_seq, D,
+                  int4 ? D / 2 : D * (int)esize(dtype)};
+  return CSA_OK;
+}
+
+static int paged_rows(const void *rows, long long row_stride, long long seq_stride, const void *pages,
+                      const uint8_t *scales, const int32_t *page_table, const int32_t *entry0, const int32_t *n_new,
+                      int B, int n, int D, int num_pages, int page_size, int pages_per_seq, int rope_dims,
+                      double rope_theta, const int64_t *pos0, int pos_stride, int dtype, int cache_dtype, bool append,
+                      void *ws, size_t ws_bytes, cudaStream_t stream) {
+  PagedRowsArgs a{};
+  int rc = check_cache(pages, scales, page_table, num_pages, page_size, pages_per_seq, D, 4096, dtype, cache_dtype,
+                       &a.cache);
+  if (rc) return rc;
+  if (B < 0 || n < 0 || (reinterpret_cast<uintptr_t>(entry0) & 3) || (reinterpret_cast<uintptr_t>(n_new) & 3))
+    return CSA_ERR_INVALID;
+  if (row_stride == 0) row_stride = D;
+  if (seq_stride == 0) seq_stride = (long long)n * row_stride;
+  if (row_stride < D || seq_stride < 0 || (!append && B > 1 && n > 0 && seq_stride < (n - 1) * row_stride + D))
+    return CSA_ERR_INVALID;
+  if (rope_dims < 0 || rope_dims > D || rope_dims % 8 ||
+      (rope_dims && (D % 2 || !(rope_theta > 1.0) || pos_stride < 0)) || (reinterpret_cast<uintptr_t>(pos0) & 7))
+    return CSA_ERR_INVALID;
+  if (!ws || !ws_aligned(ws) || ws_bytes < kStatusBytes) return CSA_ERR_WORKSPACE;
+  if (B == 0 || n == 0) return CSA_OK;
+  if (!rows || !elem_aligned(rows, dtype) || !page_table || !entry0) return CSA_ERR_INVALID;
+  if (!device_ok()) return CSA_ERR_UNSUPPORTED;
+  a.rows = rows;
+  a.entry0 = entry0;
+  a.n_new = n_new;
+  a.row_stride = row_stride;
+  a.seq_stride = seq_stride;
+  a.B = B;
+  a.n = n;
+  a.dtype = dtype;
+  a.rope_dims = rope_dims;
+  a.pos_stride = pos_stride;
+  a.rope_theta = rope_theta;
+  a.pos0 = pos0;
+  a.status = status_of(ws);
+  return cuda_rc(launch_paged_rows(a, append, stream));
+}
+
+int csa_paged_append(const void *kv, long long kv_row_stride, long long kv_seq_stride, void *pages, uint8_t *scales,
+                     const int32_t *page_table, const int32_t *entry0, const int32_t *n_new, int B, int n, int D,
+                     int num_pages, int page_size, int pages_per_seq, int rope_dims, double rope_theta,
+                     const int64_t *pos0, int pos_stride, int dtype, int cache_dtype, void *ws, size_t ws_bytes,
+                     csa_stream_t stream) {
+  return paged_rows(kv, kv_row_stride, kv_seq_stride, pages, scales, page_table, entry0, n_new, B, n, D, num_pages,
+                    page_size, pages_per_seq, rope_dims, rope_theta, pos0, pos_stride, dtype, cache_dtype, true, ws,
+                    ws_bytes, (cudaStream_t)stream);
+}
+
+int csa_paged_read(const void *pages, const uint8_t *scales, const int32_t *page_table, const int32_t *entry0,
+                   const int32_t *n_new, void *out, long long out_seq_stride, int B, int n, int D, int num_pages,
+                   int page_size, int pages_per_seq, int dtype, int cache_dtype, void *ws, size_t ws_bytes,
+                   csa_stream_t stream) {
+  return paged_rows(out, 0, out_seq_stride, pages, scales, page_table, entry0, n_new, B, n, D, num_pages, page_size,
+                    pages_per_seq, 0, 0.0, nullptr, 0, dtype, cache_dtype, false, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t csa_paged_mqa_workspace_bytes(int Q, int H, int D, int rows_max) {
+  if (Q < 1 || H < 1 || D < 1 || rows_max < 1) return kStatusBytes;
+  return kStatusBytes + align256(paged_mqa_partial_bytes(Q, H, D, rows_max));
+}
+
+static int paged_attend(const void *q, const void *pages, const uint8_t *scales, const int32_t *page_table,
+                        const int32_t *idx, const int32_t *n_cmp, const void *kv_win, const float *sink, float scale,
+                        void *out, int Q, int B, int H, int D, int num_pages, int page_size, int pages_per_seq, int k,
+                        int win_len, const int32_t *win_end, int T_raw, int q_per_seq, int dtype, int cache_dtype,
+                        void *ws, size_t ws_bytes, cudaStream_t stream) {
+  PagedMqaArgs a{};
+  int rc = check_cache(pages, scales, page_table, num_pages, page_size, pages_per_seq, D, 1024, dtype, cache_dtype,
+                       &a.cache);
+  if (rc) return rc;
+  if (!q || !sink || !out || !page_table || Q < 1 || B < 1 || H < 1 || H > 128 || q_per_seq < 1 || (long long)B * q_per_seq < Q)
+    return CSA_ERR_INVALID;
+  if (win_len < 0 || win_len > (1 << 16) ||
+      (win_len && (!kv_win || !win_end || T_raw < 1 || !elem_aligned(kv_win, dtype) ||
+                   (reinterpret_cast<uintptr_t>(win_end) & 3))))
+    return CSA_ERR_INVALID;
+  if (!elem_aligned(q, dtype) || !elem_aligned(out, dtype) || (reinterpret_cast<uintptr_t>(sink) & 3))
+    return CSA_ERR_INVALID;
+  const int32_t *list = idx ? idx : n_cmp;
+  if (!list || (reinterpret_cast<uintptr_t>(list) & 3) || (idx && (k < 1 || k > (1 << 16)))) return CSA_ERR_INVALID;
+  a.rows_max = (idx ? k : (int)a.cache.capacity()) + win_len;
+  if (!ws || !ws_aligned(ws) || ws_bytes < csa_paged_mqa_workspace_bytes(Q, H, D, a.rows_max))
+    return CSA_ERR_WORKSPACE;
+  if (!device_ok()) return CSA_ERR_UNSUPPORTED;
+  a.q = q;
+  a.kv_win = win_len ? kv_win : nullptr;
+  a.idx = idx;
+  a.n_cmp = idx ? nullptr : n_cmp;
+  a.win_end = win_len ? win_end : nullptr;
+  a.sink = sink;
+  a.out = out;
+  a.scale = scale;
+  a.Q = Q;
+  a.B = B;
+  a.H = H;
+  a.k = idx ? k : 0;
+  a.win_len = win_len;
+  a.T_raw = T_raw;
+  a.q_per_seq = q_per_seq;
+  a.dtype = dtype;
+  a.status = status_of(ws);
+  return cuda_rc(launch_paged_mqa(a, static_cast<char *>(ws) + kStatusBytes, stream));
+}
+
+int csa_paged_sparse_mqa(const void *q, const void *pages, const uint8_t *scales, const int32_t *page_table,
+                         const int32_t *idx, const void *kv_win, const float *sink, float scale, void *out, int Q,
+                         int B, int H, int D, int num_pages, int page_size, int pages_per_seq, int k, int win_len,
+                         const int32_t *win_end, int T_raw, int q_per_seq, int dtype, int cache_dtype, void *ws,
+                         size_t ws_bytes, csa_stream_t stream) {
+  if (!idx) return CSA_ERR_INVALID;
+  return paged_attend(q, pages, scales, page_table, idx, nullptr, kv_win, sink, scale, out, Q, B, H, D, num_pages,
+                      page_size, pages_per_seq, k, win_len, win_end, T_raw, q_per_seq, dtype, cache_dtype, ws, ws_bytes,
+                      (cudaStream_t)stream);
+}
+
+int csa_paged_hca_mqa(const void *q, const void *pages, const uint8_t *scales, const int32_t *page_table,
+                      const int32_t *n_cmp, const void *kv_win, const float *sink, float scale, void *out, int Q, int B,
+                      int H, int D, int num_pages, int page_size, int pages_per_seq, int win_len,
+                      const int32_t *win_end, int T_raw, int q_per_seq, int dtype, int cache_dtype, void *ws,
+                      size_t ws_bytes, csa_stream_t stream) {
+  return paged_attend(q, pages, scales, page_table, nullptr, n_cmp, kv_win, sink, scale, out, Q, B, H, D, num_pages,
+                      page_size, pages_per_seq, 0, win_len, win_end, T_raw, q_per_seq, dtype, cache_dtype, ws, ws_bytes,
+                      (cudaStream_t)stream);
 }
 
 int hca_mqa(const void *q, const void *kv_cmp, const void *kv_win, const float *sink, float scale, void *out, int Q,

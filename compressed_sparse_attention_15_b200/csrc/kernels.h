@@ -82,6 +82,29 @@ cudaError_t launch_index_compress(const CompressArgs &a, uint8_t *codes, float *
 cudaError_t launch_hadamard_rows(const void *x, void *out, uint8_t *codes, float *scales, long long rows, int D,
                                  int dtype, cudaStream_t stream);
 
+struct NormArgs {
+  const void *x, *residual;  // residual may be null
+  const float *weight;
+  void *out, *sum_out;       // out: dtype, or E4M3 codes when scales != nullptr
+  float *scales;
+  long long rows, x_stride;
+  int D, group, dtype;       // group: dims per scale (D: the row)
+  float eps;
+};
+cudaError_t launch_add_rmsnorm(const NormArgs &a, cudaStream_t stream);
+
+// The paged cache of compressed entries, as the kernels see it (paged.cuh has
+// the layout of its rows).
+struct PagedCache {
+  const uint8_t *pages;   // rows of row_bytes each, num_pages * page of them
+  const uint8_t *scales;  // 4-bit form: D / 16 bytes a row; else null
+  const int32_t *table;   // [B, per]
+  int num_pages, page, per;
+  int D, row_bytes;
+
+  __host__ __device__ long long capacity() const { return (long long)per * page; }
+};
+
 struct ScoreArgs {
   const void *qi;
   const float *wi;
@@ -200,5 +223,42 @@ int attend_call(const void *q, const void *kv_cmp, const int32_t *idx, const int
 // false when the shape or the launch plan does not allow it.
 cudaError_t launch_topk_mqa_tc(const MqaArgs &a, cudaStream_t stream, bool *taken);
 size_t mqa_partial_bytes(int Q, int H, int D, int rows_max);
+
+// ---------------------------------------------------------------- paged cache
+struct PagedRowsArgs {
+  PagedCache cache;
+  const void *rows;          // append: read; read: written
+  const int32_t *entry0, *n_new;  // n_new may be null: n rows of every sequence
+  long long row_stride, seq_stride;  // of rows, in elements
+  int B, n, dtype;
+  int rope_dims, pos_stride;
+  double rope_theta;
+  const int64_t *pos0;
+  uint32_t *status;
+};
+// append: rows into the cache; otherwise cache rows into rows.
+cudaError_t launch_paged_rows(const PagedRowsArgs &a, bool append, cudaStream_t stream);
+
+constexpr int kPagedMaxSplits = 256;  // splits of a query's row list
+
+struct PagedMqaArgs {
+  PagedCache cache;
+  const void *q, *kv_win;  // kv_win and win_end are null when win_len is 0
+  const int32_t *idx;      // null for the dense variant
+  const int32_t *n_cmp;    // dense variant: visible entries per query
+  const int32_t *win_end;
+  const float *sink;
+  void *out;
+  float scale;
+  int Q, B, H, k, win_len, T_raw, q_per_seq, dtype;
+  int rows_max;            // rows of the longest list
+  float *part_ml, *part_o; // split partials: (m, l) pairs [Q H][splits], outputs [Q H][splits][D]
+  uint32_t *status;
+};
+cudaError_t launch_paged_mqa(const PagedMqaArgs &a, void *partials, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedMqaArgs &a, int splits, cudaStream_t stream);
+size_t paged_mqa_partial_bytes(int Q, int H, int D, int rows_max);
+// Lays the partials of `splits` splits out in the workspace (sets part_ml, part_o).
+void paged_mqa_carve(PagedMqaArgs &a, void *partials, int splits);
 
 }  // namespace csa

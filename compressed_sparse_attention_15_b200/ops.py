@@ -7,12 +7,14 @@ arithmetic of the method. Names follow the C entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
 
 from . import _lib
 
+_HERE = contextlib.nullcontext()
 _DT = {torch.float32: _lib.CSA_DTYPE_F32, torch.bfloat16: _lib.CSA_DTYPE_BF16}
 
 
@@ -183,6 +185,73 @@ def hadamard_rows(x, fp8: bool = False):
                                       _lib.CSA_DTYPE_E4M3 if fp8 else _dtype_code(x), _stream(x.device))
     _lib.check("csa_hadamard_rows", rc)
     return (out, scales) if fp8 else out
+
+
+# ------------------------------------------------------- norm of the activations
+
+def _on(t: torch.Tensor):
+    """A context in which t's device is the current one (the library launches
+    on the current device)."""
+    i = t.device.index
+    return _HERE if i is None or i == torch.cuda.current_device() else torch.cuda.device(i)
+
+
+def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, fp8: bool = False, group: int = 0, out=None,
+                out_scales=None, sum_out=None):
+    """Residual addition + RMSNorm (csa_add_rmsnorm), in x's dtype or as E4M3
+    codes with one scale per ``group`` dims (32, 64, 128 or 256; 0: per row).
+
+    x: [..., D], rows contiguous and evenly spaced; weight [D] fp32; residual
+    as x. Returns a tuple: (y,), or with fp8 (codes uint8 [..., D], scales fp32
+    [..., D / group]), followed with a residual by h = x + residual (sum_out,
+    which may be residual itself)."""
+    _need(x, "x", contiguous=False)
+    dev = x.device
+    if x.dim() < 1 or x.numel() and x.stride(-1) != 1:
+        raise ValueError("x must be [..., D] with contiguous rows")
+    D = x.shape[-1]
+    _need(weight, "weight", dtype=torch.float32, device=dev)
+    if weight.shape != (D,):
+        raise ValueError("weight must be [D]")
+    if x.is_contiguous():
+        stride = 0
+    elif x.dim() == 2 and x.stride(0) >= D:
+        stride = x.stride(0)
+    else:
+        raise ValueError("x must be contiguous, or [rows, D] with rows at least D apart")
+    if residual is not None:
+        _need(residual, "residual", dtype=x.dtype, device=dev)
+        if sum_out is None:
+            sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _need(sum_out, "sum_out", dtype=x.dtype, device=dev)
+        if residual.shape != x.shape or sum_out.shape != x.shape:
+            raise ValueError("residual and sum_out must have x's shape")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    rows = x.numel() // D if D else 0
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.uint8 if fp8 else x.dtype, device=dev)
+    _need(out, "out", dtype=torch.uint8 if fp8 else x.dtype, device=dev)
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    if fp8:
+        if group and D % group:
+            raise ValueError("group must divide D")
+        if out_scales is None:
+            out_scales = torch.empty((*x.shape[:-1], D // (group or D)), dtype=torch.float32, device=dev)
+        _need(out_scales, "out_scales", dtype=torch.float32, device=dev)
+        if out_scales.shape != (*x.shape[:-1], D // (group or D)):
+            raise ValueError("out_scales must be [..., D / group]")
+    elif out_scales is not None or group:
+        raise ValueError("out_scales and group are for fp8 output")
+    code = _dtype_code(x)
+    with _on(x):
+        rc = _lib.lib().csa_add_rmsnorm(_ptr(x), stride, _ptr(residual), _ptr(weight), float(eps), _ptr(out),
+                                        _ptr(out_scales), _ptr(sum_out), rows, D, int(group), code,
+                                        _lib.CSA_DTYPE_E4M3 if fp8 else code, _stream(dev))
+    _lib.check("csa_add_rmsnorm", rc)
+    y = (out, out_scales) if fp8 else (out,)
+    return y if residual is None else (*y, sum_out)
 
 
 # ------------------------------------------------------------- A2 + A3
@@ -376,6 +445,165 @@ def hca_mqa(q, kv_cmp, n_cmp, kv_win, win_end, sink, scale: float, win_len: int,
                    _stream(q.device))
     _lib.check("hca_mqa", rc)
     return out
+
+
+# ------------------------------------------------------- paged cache
+
+def _paged(pages, scales, page_table, dtype, dev):
+    """Checks a paged cache; returns (D, num_pages, page_size, B, pages_per_seq, cache_dtype)."""
+    _need(pages, "pages", device=dev)
+    _need(page_table, "page_table", dtype=torch.int32, device=dev)
+    if pages.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("pages must be [num_pages, page_size, D] (D / 2 bytes in 4 bits), page_table [B, pages_per_seq]")
+    num_pages, page_size, D = pages.shape
+    if scales is None:
+        if pages.dtype != dtype:
+            raise TypeError(f"pages must be {dtype}, or uint8 codes with scales")
+        cache = _DT.get(dtype, -1)
+    else:
+        _need(pages, "pages", dtype=torch.uint8)
+        if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError("scales must be E4M3 (or its bytes as uint8)")
+        _need(scales, "scales", device=dev)
+        D *= 2
+        if D % 16 or scales.shape != (num_pages, page_size, D // 16):
+            raise ValueError("scales must be [num_pages, page_size, D / 16] with D a multiple of 16")
+        cache = _lib.CSA_CACHE_INT4
+    return D, num_pages, page_size, *page_table.shape, cache
+
+
+def _paged_counts(entry0, n_new, B, dev):
+    for t, nm in ((entry0, "entry0"), (n_new, "n_new")):
+        if t is not None or nm == "entry0":
+            _need(t, nm, dtype=torch.int32, device=dev)
+            if t.shape != (B,):
+                raise ValueError(f"{nm} must be [B]")
+
+
+def paged_append(kv, pages, scales, page_table, entry0, n_new=None, rope=None, ws: Workspace | None = None):
+    """Rows into a paged cache (csa_paged_append): row i < n_new[b] of kv[b] becomes entry entry0[b] + i.
+
+    kv: [B, n, D], rows contiguous, any row and sequence stride. pages
+    [num_pages, page_size, D] of kv's dtype with scales None, or uint8
+    [num_pages, page_size, D / 2] with scales [num_pages, page_size, D / 16]
+    (E4M3 or uint8); page_table int32 [B, pages_per_seq]; entry0, n_new int32
+    [B]. rope = (rope_dims, theta, pos0 int64 [B] or None, pos_stride) rotates
+    each row's last rope_dims dims for position pos0[b] + i * pos_stride.
+    Returns pages."""
+    _need(kv, "kv", contiguous=False)
+    dev, code = kv.device, _dtype_code(kv)
+    D, num_pages, page_size, B, per, cache = _paged(pages, scales, page_table, kv.dtype, dev)
+    if kv.dim() != 3 or kv.shape[0] != B or kv.shape[2] != D:
+        raise ValueError("kv must be [B, n, D]")
+    n = kv.shape[1]
+    rs, ss = (kv.stride(1) if n > 1 else D), (kv.stride(0) if B > 1 else 0)
+    if kv.numel() and (kv.stride(2) != 1 and D > 1 or rs < D or B > 1 and ss < 1):
+        raise ValueError("kv must have contiguous rows, at least D apart, and a positive sequence stride")
+    _paged_counts(entry0, n_new, B, dev)
+    rope_dims, theta, pos0, pos_stride = rope or (0, 0.0, None, 0)
+    if pos0 is not None:
+        _need(pos0, "pos0", dtype=torch.int64, device=dev)
+        if pos0.shape != (B,):
+            raise ValueError("pos0 must be [B]")
+    with _on(kv):
+        w = (ws or Workspace(dev)).get(256)
+        rc = _lib.lib().csa_paged_append(
+            _ptr(kv), max(rs, 0), max(ss, 0), _ptr(pages), _ptr(scales), _ptr(page_table), _ptr(entry0), _ptr(n_new), B, n,
+            D, num_pages, page_size, per, int(rope_dims), float(theta), _ptr(pos0), int(pos_stride), code, cache, _ptr(w),
+            w.numel(), _stream(dev))
+    _lib.check("csa_paged_append", rc)
+    return pages
+
+
+def paged_read(pages, scales, page_table, entry0, n: int, n_new=None, out=None, dtype=None, ws: Workspace | None = None):
+    """Cache rows back as values (csa_paged_read): [B, n, D], row i < n_new[b]
+    of sequence b being entry entry0[b] + i. Rows past n_new are left as they
+    were in ``out`` (zero when allocated here, in ``dtype``: bf16 by default
+    for a 4-bit cache). out: rows contiguous, any sequence stride."""
+    _need(pages, "pages")
+    dev = pages.device
+    if out is not None:
+        _need(out, "out", device=dev, contiguous=False)
+        dtype = out.dtype
+    elif dtype is None:
+        dtype = torch.bfloat16 if scales is not None else pages.dtype
+    D, num_pages, page_size, B, per, cache = _paged(pages, scales, page_table, dtype, dev)
+    if out is None:
+        out = torch.zeros((B, int(n), D), dtype=dtype, device=dev)
+    if out.shape != (B, n, D) or out.numel() and (D > 1 and out.stride(2) != 1 or n > 1 and out.stride(1) != D):
+        raise ValueError("out must be [B, n, D] with contiguous [n, D] rows")
+    _paged_counts(entry0, n_new, B, dev)
+    with _on(pages):
+        w = (ws or Workspace(dev)).get(256)
+        rc = _lib.lib().csa_paged_read(
+            _ptr(pages), _ptr(scales), _ptr(page_table), _ptr(entry0), _ptr(n_new), _ptr(out),
+            out.stride(0) if B > 1 else 0, B, int(n), D, num_pages, page_size, per, _dtype_code(out), cache, _ptr(w),
+            w.numel(), _stream(dev))
+    _lib.check("csa_paged_read", rc)
+    return out
+
+
+def _paged_mqa(name, q, pages, scales, page_table, rows, kv_win, win_end, sink, scale, win_len, q_per_seq, out, ws):
+    _need(q, "q")
+    dev, code = q.device, _dtype_code(q)
+    if q.dim() != 3:
+        raise ValueError("q must be [Q, H, D]")
+    Q, H, D = q.shape
+    D2, num_pages, page_size, B, per, cache = _paged(pages, scales, page_table, q.dtype, dev)
+    _need(sink, "sink", dtype=torch.float32, device=dev)
+    _need(rows, "idx" if name == "csa_paged_sparse_mqa" else "n_cmp", dtype=torch.int32, device=dev)
+    if D2 != D or sink.shape != (H,) or rows.shape[:1] != (Q,):
+        raise ValueError("shape mismatch among q [Q,H,D], pages [P,page,D], sink [H], idx [Q,k] or n_cmp [Q]")
+    T_raw = 0
+    if win_len:
+        _need(kv_win, "kv_win", dtype=q.dtype, device=dev)
+        _need(win_end, "win_end", dtype=torch.int32, device=dev)
+        if kv_win.dim() != 3 or kv_win.shape[0] != B or kv_win.shape[2] != D or win_end.shape != (Q,):
+            raise ValueError("kv_win must be [B, T, D] and win_end [Q]")
+        T_raw = kv_win.shape[1]
+    elif kv_win is not None or win_end is not None:
+        raise ValueError("kv_win and win_end must be None without a window")
+    if q_per_seq is None:
+        if B == 0 or Q % B:
+            raise ValueError("q_per_seq is required when B does not divide Q")
+        q_per_seq = Q // B
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", dtype=q.dtype, device=dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    L = _lib.lib()
+    k = () if name != "csa_paged_sparse_mqa" else (rows.shape[1],)
+    with _on(q):
+        nbytes = L.csa_paged_mqa_workspace_bytes(Q, H, D, (k[0] if k else per * page_size) + int(win_len))
+        w = (ws or Workspace(dev)).get(nbytes)
+        rc = getattr(L, name)(
+            _ptr(q), _ptr(pages), _ptr(scales), _ptr(page_table), _ptr(rows), _ptr(kv_win), _ptr(sink), float(scale),
+            _ptr(out), Q, B, H, D, num_pages, page_size, per, *k, int(win_len), _ptr(win_end), T_raw, int(q_per_seq), code,
+            cache, _ptr(w), w.numel(), _stream(dev))
+    _lib.check(name, rc)
+    return out
+
+
+def paged_sparse_mqa(q, pages, scales, page_table, idx, kv_win, win_end, sink, scale: float, win_len: int,
+                     q_per_seq=None, out=None, ws: Workspace | None = None):
+    """CSA attention over the selected entries of a paged cache + window + sink
+    (csa_paged_sparse_mqa). idx int32 [Q, k]; without a window win_len is 0 and
+    kv_win, win_end None."""
+    if isinstance(idx, torch.Tensor) and idx.dim() != 2:
+        raise ValueError("idx must be [Q, k]")
+    return _paged_mqa("csa_paged_sparse_mqa", q, pages, scales, page_table, idx, kv_win, win_end, sink, scale, win_len,
+                      q_per_seq, out, ws)
+
+
+def paged_hca_mqa(q, pages, scales, page_table, n_cmp, kv_win, win_end, sink, scale: float, win_len: int,
+                  q_per_seq=None, out=None, ws: Workspace | None = None):
+    """HCA attention over every visible entry of a paged cache + window + sink
+    (csa_paged_hca_mqa). n_cmp int32 [Q]."""
+    if isinstance(n_cmp, torch.Tensor) and n_cmp.dim() != 1:
+        raise ValueError("n_cmp must be [Q]")
+    return _paged_mqa("csa_paged_hca_mqa", q, pages, scales, page_table, n_cmp, kv_win, win_end, sink, scale, win_len,
+                      q_per_seq, out, ws)
 
 
 # ------------------------------------------------------- the whole decode step

@@ -66,14 +66,18 @@ enum {
 };
 
 /* Element types of the dtype-typed tensors. */
-enum { CSA_DTYPE_F32 = 0, CSA_DTYPE_BF16 = 1, CSA_DTYPE_E4M3 = 2 /* FP8 indexer entry points only */ };
+enum { CSA_DTYPE_F32 = 0, CSA_DTYPE_BF16 = 1, CSA_DTYPE_E4M3 = 2 /* FP8 indexer entry points and csa_add_rmsnorm */ };
+
+/* Element type of a paged cache in 4 bits (cache_dtype of the csa_paged_* calls). */
+enum { CSA_CACHE_INT4 = 3 };
 
 /* Bits of the workspace status word. */
 enum {
   CSA_STATUS_BAD_COUNT = 1u,   /* an n_cmp value was < 0 or > N_max; it was clamped */
   CSA_STATUS_BAD_INDEX = 2u,   /* an idx value was < -1 or >= N_max; the row was skipped */
   CSA_STATUS_BAD_WINDOW = 4u,  /* a win_end value was < 0 or >= T_raw; it was clamped */
-  CSA_STATUS_WAIT_TIMEOUT = 8u /* a bounded pipeline wait gave up; that output is invalid */
+  CSA_STATUS_WAIT_TIMEOUT = 8u, /* a bounded pipeline wait gave up; that output is invalid */
+  CSA_STATUS_BAD_PAGE = 16u    /* a page_table value was < 0 or >= num_pages; the row was skipped */
 };
 
 /* Largest supported top-k. */
@@ -192,6 +196,34 @@ int csa_index_compress(const void *kv, const void *gate, const float *ape, const
                        csa_stream_t stream);
 int csa_hadamard_rows(const void *x, void *out, float *out_scales, long long rows, int D, int dtype, int out_dtype,
                       csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_add_rmsnorm -- the residual's addition, RMSNorm, and the 8-bit form of
+ * its result: the norm in front of a layer's projections and of the query
+ * latents ("DeepSeek-V4-Flash" model card, table "Champs bruts du
+ * config.json": rms_norm_eps 1e-6, q_lora_rank 1024; the projections are FP8
+ * E4M3 with dynamic activation scales, "deepseek-ai/DeepSeek-V4-Flash-0731",
+ * table "Config changes"). For every row:
+ *     h = x + residual, rounded to dtype (h = x without a residual)
+ *     y = h / sqrt(mean_d h[d]^2 + eps) * weight          (fp32)
+ * sum_out (with a residual) takes h. out_dtype = dtype: out takes y, rounded
+ * once. out_dtype = CSA_DTYPE_E4M3: out takes E4M3 codes (uint8) and
+ * out_scales one float32 scale per `group` consecutive dims (0: per row),
+ * [rows, D / group]: scale = amax|y| / 448 over the group (1 for a zero
+ * group), code = E4M3(y / scale), nearest even, saturating (csa_hadamard_rows'
+ * encoding). A NaN gives NaN; an infinity gives NaN in its place and 0 elsewhere.
+ *   x       : [rows, D] dtype, rows x_stride elements apart (0 means D).
+ *   residual, sum_out, out : [rows, D], dense. sum_out may be residual or x
+ *             (with x_stride D); out may be x or residual (same type); no
+ *             other overlap.
+ *   weight  : [D] float32.
+ * Limits: 1 <= D <= 16384, eps >= 0, group 0 or one of 32, 64, 128, 256 that
+ * divides D (E4M3 only). rows = 0 does nothing. Returns CSA_ERR_INVALID before
+ * any launch.
+ * ---------------------------------------------------------------------- */
+int csa_add_rmsnorm(const void *x, long long x_stride, const void *residual, const float *weight, float eps, void *out,
+                    float *out_scales, void *sum_out, long long rows, int D, int group, int dtype, int out_dtype,
+                    csa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * csa_index_topk -- indexer scores and top-k selection of compressed entries.
@@ -450,6 +482,93 @@ enum { CSA_STEP_CHAINED = 0, CSA_STEP_PERSISTENT = 1 };
 
 size_t csa_decode_step_workspace_bytes(const csa_decode_step_args *args);
 int csa_decode_step(const csa_decode_step_args *args, void *ws, size_t ws_bytes, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The paged cache: csa_paged_append, csa_paged_read and, below,
+ * csa_paged_sparse_mqa and csa_paged_hca_mqa -- compressed entries (or any
+ * rows with K = V) kept in pages that a page table assigns to sequences.
+ *
+ * Entry e of sequence b lies in page page_table[b, e / page_size] at row
+ * e % page_size. cache_dtype = dtype keeps rows as they are; cache_dtype =
+ * CSA_CACHE_INT4 keeps every 16 consecutive dims as 4-bit codes under one
+ * E4M3 scale: 288 bytes for 512 dims, where bf16 takes 1,024.
+ *     s = E4M3(amax|v| / 7)  (nearest even, at most 448)
+ *     c = 8 + clamp(rint(v / s), -7, 7)   (rint: ties to even; 8 when s is 0)
+ * and (s, c) stands for (c - 8) s, which bf16 holds exactly. A NaN makes its
+ * group's scale NaN and every code 8; infinities saturate.
+ *   pages      : [num_pages, page_size, D] dtype, or [num_pages, page_size,
+ *                D / 2] uint8: 4 bytes hold 8 dims, as a little-endian 32-bit
+ *                word with dims 0, 2, 4, 6 in the nibbles of its low half
+ *                (lowest first) and dims 1, 3, 5, 7 in those of its high half.
+ *   scales     : [num_pages, page_size, D / 16] E4M3 (4 bits), else NULL.
+ *   page_table : [B, pages_per_seq] int32 device array. A page may stand in
+ *                several tables (a shared prefix); what two rows of one
+ *                append write to the same place is either's.
+ *   page_size  : any size >= 1.
+ * pages_per_seq * page_size is the capacity of a sequence (up to 2^31 - 2^20
+ * entries). Offsets are 64-bit. A code page is 8-byte aligned and D a multiple
+ * of 16 (4 bits).
+ *
+ * csa_paged_append: row i < n_new[b] of sequence b becomes entry entry0[b] + i.
+ *   With rope_dims > 0 its last rope_dims dims are rotated on the way, in
+ *   adjacent pairs (d, d + 1), pair j by the angle
+ *       (pos0[b] + i * pos_stride) * rope_theta^(-2 j / rope_dims)
+ *   (formed and applied in double precision), and rounded to dtype before
+ *   they are stored or quantised: what csa_compress_rope would have stored.
+ *   kv      : [B, n, D] dtype, rows kv_row_stride elements apart (0: D),
+ *             sequences kv_seq_stride apart (0: n * row stride).
+ *   entry0  : [B] int32.   n_new : [B] int32 (0 .. n) or NULL (n everywhere).
+ *   pos0    : [B] int64 or NULL (zeros). pos_stride >= 0: tokens per entry.
+ *   rope_dims a multiple of 8, <= D (0: none; the rest is then not read);
+ *   D even and rope_theta > 1 with it.
+ * csa_paged_read: the inverse: out[b, i] = values of entry entry0[b] + i for
+ *   i < n_new[b]; rows from n_new[b] on are left as they were.
+ *   out     : [B, n, D] dtype, dense rows, sequences out_seq_stride apart (0:
+ *             n * D).
+ * An entry outside the capacity raises CSA_STATUS_BAD_INDEX, a page outside
+ * the pool CSA_STATUS_BAD_PAGE (the row is skipped), a bad n_new
+ * CSA_STATUS_BAD_COUNT (clamped). Limits: D <= 4096; B = 0 or n = 0 does
+ * nothing. ws: the 256-byte status page suffices.
+ * ---------------------------------------------------------------------- */
+int csa_paged_append(const void *kv, long long kv_row_stride, long long kv_seq_stride, void *pages, uint8_t *scales,
+                     const int32_t *page_table, const int32_t *entry0, const int32_t *n_new, int B, int n, int D,
+                     int num_pages, int page_size, int pages_per_seq, int rope_dims, double rope_theta,
+                     const int64_t *pos0, int pos_stride, int dtype, int cache_dtype, void *ws, size_t ws_bytes,
+                     csa_stream_t stream);
+int csa_paged_read(const void *pages, const uint8_t *scales, const int32_t *page_table, const int32_t *entry0,
+                   const int32_t *n_new, void *out, long long out_seq_stride, int B, int n, int D, int num_pages,
+                   int page_size, int pages_per_seq, int dtype, int cache_dtype, void *ws, size_t ws_bytes,
+                   csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_paged_sparse_mqa, csa_paged_hca_mqa -- csa_sparse_mqa's and hca_mqa's
+ * attention over entries of a paged cache (bf16, fp32 or 4 bits), read where
+ * they lie: the rows are the entries idx[q, :] (>= 0; -1 is an unused slot)
+ * or the entries below n_cmp[q] of sequence q / q_per_seq, and the window
+ * rows of kv_win, in dtype, as there. Differences from those calls:
+ *   win_len = 0 (with kv_win, win_end NULL) attends without a window.
+ *   H 1 .. 128, D <= 1024, k and win_len up to 65,536.
+ *   A query without any row gives 0 (with a sink of -infinity too).
+ *   An entry given twice in idx counts twice.
+ * Device-side faults as above (CSA_STATUS_BAD_INDEX, _BAD_PAGE, _BAD_COUNT,
+ * _BAD_WINDOW): the row is skipped, the count or window end clamped.
+ * Entries past n_cmp, unlisted entries and rows outside the window are never
+ * read: what lies there (a NaN, say) has no effect.
+ * Workspace: csa_paged_mqa_workspace_bytes(Q, H, D, rows), rows = k + win_len
+ * or pages_per_seq * page_size + win_len. Calls that share one must not
+ * overlap on the GPU.
+ * ---------------------------------------------------------------------- */
+size_t csa_paged_mqa_workspace_bytes(int Q, int H, int D, int rows_max);
+int csa_paged_sparse_mqa(const void *q, const void *pages, const uint8_t *scales, const int32_t *page_table,
+                         const int32_t *idx, const void *kv_win, const float *sink, float scale, void *out, int Q,
+                         int B, int H, int D, int num_pages, int page_size, int pages_per_seq, int k, int win_len,
+                         const int32_t *win_end, int T_raw, int q_per_seq, int dtype, int cache_dtype, void *ws,
+                         size_t ws_bytes, csa_stream_t stream);
+int csa_paged_hca_mqa(const void *q, const void *pages, const uint8_t *scales, const int32_t *page_table,
+                      const int32_t *n_cmp, const void *kv_win, const float *sink, float scale, void *out, int Q, int B,
+                      int H, int D, int num_pages, int page_size, int pages_per_seq, int win_len,
+                      const int32_t *win_end, int T_raw, int q_per_seq, int dtype, int cache_dtype, void *ws,
+                      size_t ws_bytes, csa_stream_t stream);
 
 /* Number of kernels this library has launched in this process so far
  * (a monotonically increasing counter, for profiling and tests). */
