@@ -409,7 +409,8 @@ static int check_cache(const void *pages, const uint8_t *scales, const int32_t *
            : (scales || cache_dtype != dtype || !elem_aligned(pages, dtype)))
     return CSA_ERR_INVALID;
   *c = PagedCache{static_cast<const uint8_t *>(pages), scales, page_table, num_pages, page_size, pages_per_seq, D,
-                  int4 ? D / 2 : D * (int)esize(dtype)};
+                  int4 ? D / 2 : D * (int)esize(dtype), -1};
+  if ((page_size & (page_size - 1)) == 0) c->shift = __builtin_ctz(page_size);
   return CSA_OK;
 }
 

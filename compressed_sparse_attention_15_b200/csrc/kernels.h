@@ -101,6 +101,7 @@ struct PagedCache {
   const int32_t *table;   // [B, per]
   int num_pages, page, per;
   int D, row_bytes;
+  int shift;              // log2 of page, or -1
 
   __host__ __device__ long long capacity() const { return (long long)per * page; }
 };
@@ -256,6 +257,9 @@ struct PagedMqaArgs {
   uint32_t *status;
 };
 cudaError_t launch_paged_mqa(const PagedMqaArgs &a, void *partials, cudaStream_t stream);
+// The tensor-core kernel (bf16, D a multiple of 128 up to 512); *taken is false when it does not take the shape.
+cudaError_t launch_paged_mqa_tc(const PagedMqaArgs &a, void *partials, cudaStream_t stream, bool *taken);
+int paged_mqa_tc_splits(int Q, int H, int D, int rows_max);
 cudaError_t launch_paged_merge(const PagedMqaArgs &a, int splits, cudaStream_t stream);
 size_t paged_mqa_partial_bytes(int Q, int H, int D, int rows_max);
 // Lays the partials of `splits` splits out in the workspace (sets part_ml, part_o).

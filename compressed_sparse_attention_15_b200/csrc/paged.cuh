@@ -16,6 +16,12 @@
 
 namespace csa {
 
+// The page of a sequence's entry, and its row there.
+__device__ __forceinline__ uint2 page_and_row(const PagedCache &c, uint32_t e) {
+  const uint32_t pg = c.shift >= 0 ? e >> c.shift : e / (uint32_t)c.page;
+  return make_uint2(pg, e - pg * (uint32_t)c.page);
+}
+
 // Row of the flattened pages that holds entry e of sequence b; -1 with a
 // status bit where the entry or its page does not exist.
 __device__ __forceinline__ long long paged_slot(const PagedCache &c, int b, long long e, uint32_t *status) {
@@ -23,13 +29,13 @@ __device__ __forceinline__ long long paged_slot(const PagedCache &c, int b, long
     raise_status(status, CSA_STATUS_BAD_INDEX);
     return -1;
   }
-  const uint32_t pg = (uint32_t)e / (uint32_t)c.page, row = (uint32_t)e - pg * (uint32_t)c.page;
-  const int p = c.table[(size_t)b * c.per + pg];
+  const uint2 at = page_and_row(c, (uint32_t)e);
+  const int p = c.table[(size_t)b * c.per + at.x];
   if (p < 0 || p >= c.num_pages) {
     raise_status(status, CSA_STATUS_BAD_PAGE);
     return -1;
   }
-  return (long long)p * c.page + row;
+  return (long long)p * c.page + at.y;
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t u) {

@@ -3,7 +3,8 @@
 //
 // The mathematics is csa_sparse_mqa's and hca_mqa's (mqa.cu), over rows found
 // through a page table and, in the 4-bit form, widened on the way. This file
-// holds the fp32-FFMA kernel for every shape, and the merge of its splits.
+// holds the fp32-FFMA kernel for every shape, and the merge of its splits; the
+// tensor-core kernel (bf16, head_dim a multiple of 128) is in paged_mqa_tc.cu.
 //
 // One block takes HG heads of a query and one of `splits` runs of 32-row
 // chunks of its row list, and keeps the running maximum, sum and output of the
@@ -327,7 +328,8 @@ cudaError_t launch_paged_merge(const PagedMqaArgs &a, int splits, cudaStream_t s
 }
 
 size_t paged_mqa_partial_bytes(int Q, int H, int D, int rows_max) {
-  return sizeof(float) * partial_floats(Q, H, D, generic_splits(Q, H, rows_max));
+  const int s = generic_splits(Q, H, rows_max), t = paged_mqa_tc_splits(Q, H, D, rows_max);
+  return sizeof(float) * partial_floats(Q, H, D, s > t ? s : t);
 }
 
 // The workspace's partials: the (m, l) pairs, then the outputs, 16-byte aligned.
@@ -337,6 +339,9 @@ void paged_mqa_carve(PagedMqaArgs &a, void *partials, int splits) {
 }
 
 cudaError_t launch_paged_mqa(const PagedMqaArgs &args, void *partials, cudaStream_t stream) {
+  bool taken = false;
+  const cudaError_t e = launch_paged_mqa_tc(args, partials, stream, &taken);
+  if (taken) return e;
   PagedMqaArgs a = args;
   paged_mqa_carve(a, partials, generic_splits(a.Q, a.H, a.rows_max));
   return a.dtype == CSA_DTYPE_F32 ? launch_generic<float>(a, stream) : launch_generic<bf16>(a, stream);

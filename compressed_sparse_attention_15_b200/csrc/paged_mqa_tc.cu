@@ -1,0 +1,954 @@
+// csa_paged_sparse_mqa / csa_paged_hca_mqa on the tensor cores: bf16 queries,
+// head_dim 128, 256, 384 or 512, a paged cache in bf16 or 4 bits.
+//
+// The products are mqa_tc.cu's, transposed, with the heads (64 a block, unused
+// ones zero) on N:
+//   S^T[r, h]  = sum_d KV[r, d] Q[h, d]      M = 64 rows,  K-major A and B
+//   O^T[d, h] += sum_r KV[r, d] P^T[r, h]    M = 128 dims, A = the same tile read MN-major
+// and so are the online softmax (running maximum moved only when a logit passes
+// it by 2^8), the two tile buffers, and the issue order.
+//
+// A tile of 4-bit rows is widened to bf16 on its way into shared memory. One
+// packed fused multiply-add makes two values, exactly: a nibble c placed in the
+// mantissa of 128 is 128 + c, and (128 + c) s - 136 s = (c - 8) s, where s, 136 s
+// (17 times 8 to 15 eighths: 8 significant bits) and the result are bf16 numbers. A lane takes 32 bytes of a row, the 64 dims of one
+// 128-byte swizzled line, and 8 lanes take 8 rows, so that every 16-byte store
+// of theirs falls into distinct banks. The packed rows come through a staging
+// tile, which two warps fill by asynchronous copies while the tile before is
+// widened: loads into registers would have to be waited for at the fence that
+// shows a tile to the tensor core. Their lookups (list, page table) run three
+// tiles ahead, each load a tile ahead of its use.
+//
+// Two tiles are in flight (a third does not fit beside the queries), so a
+// tile's way through widening, S^T, softmax and P.V bounds the rate as much as
+// any one unit does: every widening warp works on every tile; a tile's halves (of
+// 256 dims) are handed over one by one, so that S^T starts on the first while
+// the second is widened, and the next tile's first half is widened while P.V
+// works on the second; and eight softmax warps, a quarter of the rows and half
+// of the heads each, take the logits as packed pairs, with one barrier (per half
+// of the heads) on the usual path.
+//
+// The kernel is persistent: a block takes items (one split of the row list of 64
+// heads of a query) in turn, and each role runs ahead into the next item, so that
+// its loads, its queries' and its first products overlap the end of the last.
+//
+// Roles (640 threads): warps 0-7 widen (or copy bf16 rows), warps 8-15 run the
+// softmax and write the output, warp 16 loads the queries and issues S^T, warp
+// 17 issues P.V and owns TMEM, warps 18 and 19 look rows up and fetch them. All
+// mbarrier waits are bounded; the softmax warps of a half take every decision to
+// stop together.
+#include "attn.cuh"
+#include "paged.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+
+namespace csa {
+
+namespace {
+
+constexpr int kH = 64;                              // heads per block
+constexpr int kRows = 64;                           // rows per tile
+constexpr uint32_t kBoxBytes = kRows * 128;         // 64 rows x 64 dims
+constexpr uint32_t kQBoxBytes = kH * 128;           // 64 heads x 64 dims
+constexpr uint32_t kPBytes = kRows * kH * 2;
+constexpr int kLoadWarps = 8;
+constexpr int kRowsPerWarp = kRows / kLoadWarps;    // 8
+constexpr int kSoftWarp0 = kLoadWarps;
+constexpr int kSoftWarps = 8;
+constexpr int kSWarp = kSoftWarp0 + kSoftWarps;
+constexpr int kPvWarp = kSWarp + 1;
+constexpr int kFetchWarp0 = kPvWarp + 1;
+constexpr int kThreads = 32 * (kFetchWarp0 + 2);
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kFloor = -1e30f;  // running maximum of no rows (finite: no inf - inf)
+
+struct Small {
+  // per tile buffer (and half of the dims): filled, read; per tile buffer: S^T made, P^T written
+  uint64_t kv_full[2][2], kv_empty[2][2], s_full[2];
+  uint64_t p_full;                             // P^T written
+  uint64_t stage_full, stage_empty;            // the staging tile and its slots: filled, read
+  uint64_t pv_done[4];                         // P.V made, per tile (mod 4)
+  uint64_t q_full, q_empty, o_done, o_free;    // per item: queries loaded / read, O^T made / read
+  uint64_t norm_full;                          // per item: norm is there
+  uint64_t s_fin, pv_fin;                      // the last products of the block
+  float red[4][kH];
+  float mref[kH];
+  float alpha[kH];            // what a rescale multiplies by
+  float norm[kH];             // what the item's output is multiplied by
+  uint32_t tmem_base;
+  int abort;
+  int rescale[2];             // per half of the heads
+  uint8_t valid[2][kRows];    // per tile buffer: the row holds a key
+  long long slot[kRows];      // of the staged tile: row of the window or of the pages, -1: no key
+};
+
+// The staging tile: 64 rows of codes, then of scales. Row strides that put 8
+// rows' reads (16 and 4 bytes a lane) into distinct banks.
+constexpr uint32_t stage_row(int NB) { return 32 * NB + 16; }
+constexpr uint32_t kStageScaleRow = 48;
+constexpr uint32_t stage_bytes(int NB) { return kRows * (stage_row(NB) + kStageScaleRow); }
+
+// Shared memory, in 64-dim boxes: two KV tiles, Q, P^T; the staging tile.
+constexpr size_t smem_bytes(int NB) {
+  return 1024 + (size_t)NB * (2 * kBoxBytes + kQBoxBytes) + kPBytes + stage_bytes(NB) + sizeof(Small);
+}
+static_assert(smem_bytes(8) <= 227 * 1024, "shared memory per block");
+
+// An item: a run of tiles (split blockIdx.y of gridDim.y) of the row list of 64
+// heads of a query. The list is the window rows [0, nwin) (kv_win rows wlo ...,
+// padded with unused rows to whole tiles: w64), then the compressed rows
+// [w64, w64 + nsel).
+struct Item {
+  int qq, h0, b;
+  int nsel, wlo, nwin, w64;
+  int t0, ntiles;
+};
+
+// The device values an item depends on, loaded an item ahead.
+struct Raw {
+  int n, e;
+};
+
+// Query qv / 2 and its heads 64 (qv % 2) ... where a query has more than 64 heads, else query qv.
+__device__ __forceinline__ int query_of(const PagedMqaArgs &a, int qv) { return a.H > kH ? qv >> 1 : qv; }
+
+__device__ __forceinline__ Raw load_raw(const PagedMqaArgs &a, int qv, int qvs) {
+  Raw r{a.k, 0};
+  if (qv < qvs) {
+    const int qq = query_of(a, qv);
+    if (!a.idx) r.n = a.n_cmp[qq];
+    if (a.win_len) r.e = a.win_end[qq];
+  }
+  return r;
+}
+
+__device__ __forceinline__ Item make_item(const PagedMqaArgs &a, int qv, Raw raw, uint32_t *status) {
+  Item t;
+  t.qq = query_of(a, qv);
+  t.h0 = a.H > kH ? (qv & 1) * kH : 0;
+  t.b = t.qq / a.q_per_seq;
+  t.nsel = a.idx ? a.k : clamp_count(raw.n, (int)a.cache.capacity(), status);
+  t.wlo = t.nwin = 0;
+  if (a.win_len) {
+    int e = raw.e;
+    if (e < 0 || e >= a.T_raw) {
+      raise_status(status, CSA_STATUS_BAD_WINDOW);
+      e = e < 0 ? 0 : a.T_raw - 1;
+    }
+    t.wlo = max(0, e - a.win_len + 1);
+    t.nwin = e - t.wlo + 1;
+  }
+  t.w64 = (t.nwin + kRows - 1) / kRows * kRows;
+  const int tiles = (t.w64 + t.nsel + kRows - 1) / kRows;
+  t.t0 = 0;
+  t.ntiles = tiles;
+  if (gridDim.y > 1) {
+    const int splits = gridDim.y, split = blockIdx.y, base = tiles / splits, rest = tiles - base * splits;
+    t.t0 = split * base + min(split, rest);
+    t.ntiles = base + (split < rest ? 1 : 0);
+  }
+  return t;
+}
+
+// 32 bytes of codes and 4 of scales: 64 dims of one row.
+struct Packed {
+  uint32_t w[8];
+  uint32_t s;
+};
+
+__device__ __forceinline__ void load_packed(Packed &u, uint32_t codes, uint32_t scales) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.w[4 * i]), "=r"(u.w[4 * i + 1]), "=r"(u.w[4 * i + 2]), "=r"(u.w[4 * i + 3])
+                 : "r"(codes + 16 * i));
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u.s) : "r"(scales));
+}
+
+// n bytes (8 or 16), or zeros.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_piece(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(valid ? kBytes : 0)
+               : "memory");
+}
+
+// An arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+// *p, or 0 without reading it where !pred. (One predicated load: no branch at
+// whose end its value would be waited for.)
+__device__ __forceinline__ int load_if(const int32_t *p, bool pred) {
+  int v;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.nc.b32 %0, [%1];\n\t}"
+               : "=r"(v)
+               : "l"(p), "r"((uint32_t)pred));
+  return v;
+}
+
+// Pairs of floats in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// tcgen05.ld of 16 TMEM lanes x 32 columns (16x256b shape, 4 repeats): for
+// column group c, thread t gets r[4c + e] = (lane t/4, column 8c + 2(t%4) + e)
+// and r[4c + 2 + e] = (lane t/4 + 8, same column), e = 0, 1.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// 32 TMEM lanes x 16 columns: thread i holds lane i of the warp's quarter.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit elements: lane i gives the address of row i % 8 of
+// block i / 8 and holds row i / 4, columns 2 (i % 4) and the next, of each block.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
+}
+
+// An 8 x 8 block of 16-bit elements (lane i: row i / 4, columns 2 (i % 4) and the next), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_dup(float x) {
+  const __nv_bfloat162 t = __float2bfloat162_rn(x);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// The 64 dims of `u` into the 128-byte line whose chunk 0 is at `chunk0` (16-byte chunks, swizzled).
+__device__ __forceinline__ void store_widened(const Packed &u, uint32_t chunk0) {
+  // per 16 dims: s and -136 s, in both halves of a register
+  uint32_t sc[4], off[4];
+  if (((u.s | (u.s + 0x01010101u)) & 0x80808080u) == 0) {
+    // E4M3's exponent and mantissa, moved to where bf16 has them, are s 2^-120 (subnormals too)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t t = __byte_perm(u.s, 0, 0x4040u | (0x0101u * g)) << 4;
+      sc[g] = mul_bf16x2(t, 0x7b807b80u);   // 2^120
+      off[g] = mul_bf16x2(t, 0xff08ff08u);  // -136 2^120
+    }
+  } else {  // a NaN or a sign among the scales
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float s = e4m3_value((uint8_t)(u.s >> (8 * g)));
+      sc[g] = bf16x2_dup(s);
+      off[g] = bf16x2_dup(-136.f * s);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t w = u.w[c];
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = fma_bf16x2(((w >> (4 * k)) & 0x000f000fu) | 0x43004300u, sc[c >> 1], off[c >> 1]);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk0 ^ (c << 4)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+  }
+}
+
+// The products of dims [256 part, 256 part + 256) of one tile.
+template <int NB>
+__device__ __forceinline__ void issue_s(uint32_t tmem_s, uint64_t kv, uint64_t q, int part) {
+  constexpr uint32_t idesc = tc::idesc_bf16(64, 64, 0, 0);
+  kv += (uint64_t)((part * 4 * kBoxBytes) >> 4);
+  q += (uint64_t)((part * 4 * kQBoxBytes) >> 4);
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < 4 * NB - 16 * part)
+      tc::mma_bf16(tmem_s, kv + (uint64_t)(((j >> 2) * kBoxBytes + (j & 3) * 32) >> 4),
+                   q + (uint64_t)(((j >> 2) * kQBoxBytes + (j & 3) * 32) >> 4), idesc, part > 0 || j > 0);
+}
+template <int NB>
+__device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint64_t v, uint64_t p, bool first, int part) {
+  constexpr uint32_t idesc = tc::idesc_bf16(128, 64, 1, 1);
+  tmem_o += 128 * part;
+  v += (uint64_t)((part * 4 * kBoxBytes) >> 4);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    if (m < NB / 2 - 2 * part) {
+#pragma unroll
+      for (int j = 0; j < kRows / 16; ++j)
+        tc::mma_bf16(tmem_o + 64 * m, v + (uint64_t)((2 * m * kBoxBytes + j * 2048) >> 4), p + (uint64_t)((j * 2048) >> 4),
+                     idesc, j > 0 || !first);
+    }
+  }
+}
+
+// O^T of 64 heads of a query, [32 i, 32 i + 32) of every 128 dims and `heads`
+// (up to 32) heads from the query's `qh` on, times norm, to the output or, as it
+// is, to the partials. A warp takes blocks m0 .. m1 - 1 of 16 dims (m / 2: the
+// 128-dim chunk, m % 2: half of the warp's TMEM quarter), each turned in registers
+// so that 4 lanes write a 32-byte sector of a head's row.
+template <int NB>
+__device__ __forceinline__ void write_out(const PagedMqaArgs &a, uint32_t tmem, const float *norm, size_t qh, int heads,
+                                          int quarter, int m0, int m1, bool some, uint64_t *o_free) {
+  constexpr int kD = 64 * NB;
+  const int lane = threadIdx.x & 31, rq = lane >> 2, cq = lane & 3;
+  const int splits = gridDim.y;
+  uint64_t f[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) f[c] = pack2(norm[8 * c + 2 * cq], norm[8 * c + 2 * cq + 1]);
+#pragma unroll 1
+  for (int m = m0; m < m1; ++m) {
+    uint32_t v[16];
+    if (some) {
+      tmem_ld_16x256b_x4(tmem + ((uint32_t)(32 * quarter + 16 * (m & 1)) << 16) + 64 * (m >> 1), v);
+      tc::tmem_ld_wait();
+      if (m == m1 - 1) {  // read: the next item's P.V may overwrite it
+        tc::fence_before_sync();
+        tc::mbar_arrive(o_free);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) v[c] = 0u;
+    }
+    const int d0 = 128 * (m >> 1) + 32 * quarter + 16 * (m & 1);
+    if (splits > 1) {
+      float *po = a.part_o + ((qh + 2 * cq) * splits + blockIdx.y) * kD + d0 + rq;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (8 * c + 2 * cq + e < heads) {
+            float *p = po + (size_t)(8 * c + e) * splits * kD;
+            p[0] = __uint_as_float(v[4 * c + e]);
+            p[8] = __uint_as_float(v[4 * c + 2 + e]);
+          }
+    } else {
+      // lane 4 h + i: dims 0, 8, 4 or 12 and the next three of head 8 c + h
+      bf16 *out = static_cast<bf16 *>(a.out) + (qh + rq) * kD + d0 + 8 * (cq & 1) + 2 * (cq & 2);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t t[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 y = unpack2(mul2(pack2(__uint_as_float(v[4 * c + 2 * r]), __uint_as_float(v[4 * c + 2 * r + 1])), f[c]));
+          const __nv_bfloat162 w = __floats2bfloat162_rn(y.x, y.y);
+          t[r] = transpose8(*reinterpret_cast<const uint32_t *>(&w));  // dims 8 r + 2 cq, + 1 of head 8 c + rq
+        }
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, cq & 1 ? t[0] : t[1], 1);
+        if (8 * c + rq < heads)
+          *reinterpret_cast<uint2 *>(out + (size_t)8 * c * kD) = cq & 1 ? make_uint2(got, t[1]) : make_uint2(t[0], got);
+      }
+    }
+  }
+}
+
+// NB: head_dim / 64. kInt4: the cache is in 4 bits.
+template <int NB, bool kInt4>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_mqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, PagedMqaArgs a, int qvs, float scale_log2) {
+  constexpr int kD = 64 * NB;
+  constexpr uint32_t kTileBytes = NB * kBoxBytes, kQBytes = NB * kQBoxBytes;
+  constexpr uint32_t kColS = 64 * (NB / 2);  // O^T chunk m at columns 64 m, S^T buffer j at kColS + 64 j
+  constexpr uint32_t kTmemCols = kColS + 128 > 256 ? 512 : 256;
+  constexpr int kParts = (NB + 3) / 4;       // parts of 256 dims a tile is handed over in
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *kv = smem;                              // [2 tiles][NB boxes][64 rows][128 B]
+  uint8_t *qs = smem + 2 * kTileBytes;             // [NB boxes][64 heads][128 B]
+  uint8_t *ps = qs + kQBytes;                      // [64 rows][128 B]  (P^T, MN-major)
+  uint8_t *stage = ps + kPBytes;
+  Small *sm = reinterpret_cast<Small *>(stage + stage_bytes(NB));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      for (int j = 0; j < 2; ++j) {
+        tc::mbar_init(&sm->kv_full[i][j], 32 * kLoadWarps);
+        tc::mbar_init(&sm->kv_empty[i][j], 1);
+      }
+      tc::mbar_init(&sm->s_full[i], 1);
+    }
+    tc::mbar_init(&sm->p_full, 32 * kSoftWarps);
+    tc::mbar_init(&sm->stage_full, 2 * kRows);  // each fetching lane arrives, and so do its copies
+    tc::mbar_init(&sm->stage_empty, kLoadWarps);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&sm->pv_done[i], 1);
+    tc::mbar_init(&sm->q_full, 1);
+    tc::mbar_init(&sm->q_empty, 1);
+    tc::mbar_init(&sm->o_done, 1);
+    tc::mbar_init(&sm->o_free, 32 * (kLoadWarps + kSoftWarps));
+    tc::mbar_init(&sm->norm_full, kH);
+    tc::mbar_init(&sm->s_fin, 1);
+    tc::mbar_init(&sm->pv_fin, 1);
+    sm->abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (threadIdx.x < kH) sm->mref[threadIdx.x] = kFloor;
+  if (warp == kPvWarp) tc::tmem_alloc(&sm->tmem_base, kTmemCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sm->tmem_base;
+  volatile int *abort = &sm->abort;
+  pdl_wait();
+  const uint64_t lim = tc::wait_limit_of(a.status);
+  pdl_release();
+  Raw raw = load_raw(a, blockIdx.x, qvs);
+
+  if (warp < kLoadWarps) {
+    // ------------------------------------------------------------ widening
+    // Every warp takes 8 rows of every tile, a lane 64 dims of row lane % 8.
+    const uint32_t kv_base = tc::smem_u32(kv), stage_base = tc::smem_u32(stage);
+    const int my_row = kRowsPerWarp * warp + (lane & 7);
+    const uint32_t codes = stage_base + my_row * stage_row(NB), scales = stage_base + kRows * stage_row(NB) + my_row * kStageScaleRow;
+    uint32_t T = 0;  // tiles so far
+    bool ok = true;
+    // Half of an item's output is these warps' to write. They do so when both
+    // tile buffers hold tiles of the items after it, and have nothing else to do.
+    int out_qv = -1;
+    uint32_t out_at = 0, done = 0;  // the tile before which it is written; items written
+    auto output = [&] {
+      ok = ok && tc::mbar_wait(&sm->norm_full, done & 1, abort, a.status, lim);
+      ok = ok && tc::mbar_wait(&sm->o_done, done & 1, abort, a.status, lim);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+      const int half = warp >> 2, h0 = (a.H > kH ? (out_qv & 1) * kH : 0) + 32 * half;
+      if (ok)
+        write_out<NB>(a, tmem + 32 * half, sm->norm + 32 * half, (size_t)query_of(a, out_qv) * a.H + h0, a.H - h0, warp & 3,
+                      NB / 2, NB, true, &sm->o_free);
+      ++done;
+      out_qv = -1;
+    };
+    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
+      const Item L = make_item(a, qv, raw, nullptr);
+      raw = load_raw(a, qv + gridDim.x, qvs);
+      for (int li = 0; li < L.ntiles; ++li, ++T) {
+        const int g = T & 1;
+        if (out_qv >= 0 && T == out_at) output();
+        if (!ok) break;
+        const uint32_t free_phase = ((T >> 1) & 1) ^ 1, line = kv_base + g * kTileBytes + my_row * 128 + ((lane & 7) << 4);
+        const bool in_win = (L.t0 + li) * kRows < L.w64;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->stage_full, T & 1, abort, a.status, lim));
+        if (!ok) break;
+        const long long slot = sm->slot[my_row];
+        if (kInt4 && !in_win) {
+          Packed u[kParts];
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            const int s = min((lane >> 3) + 4 * i, NB - 1);  // (a piece past the row is not stored)
+            load_packed(u[i], codes + 32 * s, scales + 4 * s);
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm->stage_empty);
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->kv_empty[g][i], free_phase, abort, a.status, lim));
+            if (!ok) break;
+            if (i == 0 && lane < kRowsPerWarp) sm->valid[g][my_row] = slot >= 0;
+            const int s = (lane >> 3) + 4 * i;
+            if (s < NB) store_widened(u[i], line + s * kBoxBytes);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc::mbar_arrive(&sm->kv_full[g][i]);
+          }
+        } else {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm->stage_empty);
+#pragma unroll
+          for (int i = 0; i < kParts; ++i)
+            ok = ok && tc::mbar_wait(&sm->kv_empty[g][i], free_phase, abort, a.status, lim);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            if (lane < kRowsPerWarp) sm->valid[g][my_row] = slot >= 0;
+            const bf16 *base = in_win ? static_cast<const bf16 *>(a.kv_win) + (size_t)L.b * a.T_raw * kD
+                                      : reinterpret_cast<const bf16 *>(a.cache.pages);
+#pragma unroll 4
+            for (int rw = 0; rw < kRowsPerWarp; ++rw) {
+              const long long at = __shfl_sync(0xffffffffu, slot, rw);
+              const uint32_t dst = kv_base + g * kTileBytes + (kRowsPerWarp * warp + rw) * 128;
+              const bf16 *src = at >= 0 ? base + (size_t)at * kD : static_cast<const bf16 *>(a.q);
+              for (int c16 = lane; c16 < 8 * NB; c16 += 32)  // 16-byte piece c16 of the row
+                cp_async16(dst + (c16 >> 3) * kBoxBytes + (((c16 & 7) ^ rw) << 4), at >= 0 ? src + c16 * 8 : src, at >= 0);
+            }
+            cp_async_wait_all();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) tc::mbar_arrive(&sm->kv_full[g][i]);
+          }
+        }
+        if (!ok) break;
+      }
+      if (ok && L.ntiles > 0) {
+        // (an item of one tile may end before the output of the one before it is due)
+        if (out_qv >= 0) output();
+        out_qv = qv;
+        out_at = T + 2;
+      }
+    }
+    if (out_qv >= 0) output();
+  } else if (warp >= kFetchWarp0) {
+    // ------------------------------------------------------------ lookups and fetches
+    // A lane looks one row up; a warp copies its 32 rows.
+    const int half = warp - kFetchWarp0, my_row = 32 * half + lane;
+    const uint32_t codes = tc::smem_u32(stage), scales = codes + kRows * stage_row(NB);
+    uint32_t T = 0;
+    bool ok = true;
+    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
+    const Item L = make_item(a, qv, raw, nullptr);
+    raw = load_raw(a, qv + gridDim.x, qvs);
+    const int t0 = L.t0, ntiles = L.ntiles, b = L.b, qq = L.qq;
+    auto is_win = [&](int li) { return (t0 + li) * kRows < L.w64; };
+    // The lookup of this lane's row of tile li in three steps, each one load: the
+    // row's entry, or number in the window; ...
+    struct Entry {
+      int j;
+      bool live;
+    };
+    auto entry_of = [&](int li) -> Entry {
+      const int r = (t0 + li) * kRows + my_row, p = r - L.w64;
+      const bool mine = li < ntiles;
+      if (p < 0) return Entry{L.wlo + r, mine && r < L.nwin};
+      const bool live = mine && p < L.nsel;
+      return Entry{a.idx ? load_if(a.idx + (size_t)qq * a.k + p, live) : p, live};
+    };
+    // ... its page and the row there (-1: no key); ...
+    auto page_of = [&](int li, Entry e) -> int2 {
+      if (is_win(li)) return make_int2(0, e.live ? e.j : -1);
+      const bool ok = e.live && e.j >= 0 && e.j < a.cache.capacity();
+      if (e.live && !ok && e.j != -1) raise_status(a.status, CSA_STATUS_BAD_INDEX);
+      const uint2 at = page_and_row(a.cache, ok ? e.j : 0);
+      return make_int2(load_if(a.cache.table + (size_t)b * a.cache.per + at.x, ok), ok ? (int)at.y : -1);
+    };
+    // ... and the row of the window or of the pages.
+    auto row_of = [&](int li, int2 pg) -> long long {
+      if (pg.y < 0 || is_win(li)) return pg.y;
+      if (pg.x < 0 || pg.x >= a.cache.num_pages) {
+        raise_status(a.status, CSA_STATUS_BAD_PAGE);
+        return -1;
+      }
+      return (long long)pg.x * a.cache.page + pg.y;
+    };
+    const Entry e0 = entry_of(0), e1 = entry_of(1);
+    Entry e2 = entry_of(2);
+    const int2 p0 = page_of(0, e0);
+    int2 p1 = page_of(1, e1);
+    long long at = row_of(0, p0);
+    for (int li = 0; li < ntiles; ++li, ++T) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->stage_empty, (T & 1) ^ 1, abort, a.status, lim));
+      if (!ok) break;
+      sm->slot[my_row] = at;
+      if (kInt4 && !is_win(li)) {
+        constexpr int kPer = 2 * NB;  // 16-byte pieces of a row's codes
+#pragma unroll 4
+        for (int i = 0; i < kPer; ++i) {
+          const int n = 32 * i + lane, rw = n / kPer, c = n - rw * kPer;
+          const long long slot = __shfl_sync(0xffffffffu, at, rw);
+          const uint8_t *src = a.cache.pages + (slot >= 0 ? (size_t)slot * (kD / 2) + 16 * c : 0);
+          cp_async16(codes + (32 * half + rw) * stage_row(NB) + 16 * c, src, slot >= 0);
+        }
+        constexpr int kPiece = NB % 4 ? 8 : 16, kPerS = 4 * NB / kPiece;  // pieces of a row's scales
+#pragma unroll
+        for (int i = 0; i < kPerS; ++i) {
+          const int n = 32 * i + lane, rw = n / kPerS, c = n - rw * kPerS;
+          const long long slot = __shfl_sync(0xffffffffu, at, rw);
+          const uint8_t *src = a.cache.scales + (slot >= 0 ? (size_t)slot * (kD / 16) + kPiece * c : 0);
+          cp_async_piece<kPiece>(scales + (32 * half + rw) * kStageScaleRow + kPiece * c, src, slot >= 0);
+        }
+      } else if (at >= 0) {  // a bf16 row: into L2, for the copy
+        const bf16 *base = is_win(li) ? static_cast<const bf16 *>(a.kv_win) + (size_t)b * a.T_raw * kD
+                                      : reinterpret_cast<const bf16 *>(a.cache.pages);
+        bulk_prefetch_l2(base + (size_t)at * kD, kD * 2);
+      }
+      cp_async_arrive(&sm->stage_full);
+      tc::mbar_arrive(&sm->stage_full);
+      at = row_of(li + 1, p1);
+      p1 = page_of(li + 2, e2);
+      e2 = entry_of(li + 3);
+    }
+    }
+    cp_async_wait_all();  // (nothing is in flight when the block ends)
+  } else if (warp == kSWarp) {
+    // ------------------------------------------------------------ queries, S^T
+    // (the whole warp runs the loops of the two issuers; one lane issues)
+    const uint64_t ad_kv = tc::sw128_desc(tc::smem_u32(kv), 16, 1024), bd_q = tc::sw128_desc(tc::smem_u32(qs), 16, 1024);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, a.status, lim));
+    };
+    uint32_t T = 0, done = 0;  // tiles and items (with tiles) so far
+    bool ok = true;
+    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
+      const Item it = make_item(a, qv, raw, nullptr);
+      raw = load_raw(a, qv + gridDim.x, qvs);
+      if (it.ntiles == 0) continue;
+      if (done > 0 && !(ok = wait(&sm->q_empty, (done - 1) & 1))) break;
+      if (tc::elect_one()) {
+        tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
+        for (int bx = 0; bx < NB; ++bx) tc::tma_load_3d(qs + bx * kQBoxBytes, &tm_q, bx * 64, it.h0, it.qq, &sm->q_full);
+      }
+      __syncwarp();
+      if (!(ok = wait(&sm->q_full, done & 1))) {
+        if (tc::elect_one()) tc::mbar_drain(&sm->q_full, done & 1);  // (nothing is in flight when the block ends)
+        break;
+      }
+      for (int li = 0; li < it.ntiles; ++li, ++T) {
+        const int buf = T & 1;
+        // (S^T(T) overwrites S^T(T - 2), which has been read: the tile buffer was free for tile T only
+        // after P.V(T - 2))
+#pragma unroll 1
+        for (int i = 0; i < kParts; ++i) {
+          if (!(ok = wait(&sm->kv_full[buf][i], (T >> 1) & 1))) break;
+          tc::fence_after_sync();
+          if (tc::elect_one())
+            issue_s<NB>(tmem + kColS + 64 * buf, ad_kv + (uint64_t)((buf * kTileBytes) >> 4), bd_q, i);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (tc::elect_one()) {
+          tc::commit(&sm->s_full[buf]);
+          if (li == it.ntiles - 1) tc::commit(&sm->q_empty);
+        }
+        __syncwarp();
+      }
+      ++done;
+    }
+    if (tc::elect_one()) {
+      tc::commit(&sm->s_fin);
+      tc::mbar_drain(&sm->s_fin, 0);
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------ P.V
+    const uint64_t ad_v = tc::sw128_desc(tc::smem_u32(kv), kBoxBytes, 1024);
+    const uint64_t bd_p = tc::sw128_desc(tc::smem_u32(ps), kPBytes, 1024);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, a.status, lim));
+    };
+    uint32_t T = 0, done = 0;
+    bool ok = true;
+    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
+      const int ntiles = make_item(a, qv, raw, nullptr).ntiles;
+      raw = load_raw(a, qv + gridDim.x, qvs);
+      if (ntiles == 0) continue;
+      if (done > 0 && !(ok = wait(&sm->o_free, (done - 1) & 1))) break;
+      for (int li = 0; li < ntiles; ++li, ++T) {
+        const int buf = T & 1;
+        for (int i = 0; i < kParts; ++i) ok = ok && wait(&sm->kv_full[buf][i], (T >> 1) & 1);  // (the tile's writes)
+        if (!ok || !(ok = wait(&sm->p_full, T & 1))) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            issue_pv<NB>(tmem, ad_v + (uint64_t)((buf * kTileBytes) >> 4), bd_p, li == 0, i);
+            tc::commit(&sm->kv_empty[buf][i]);
+          }
+          tc::commit(&sm->pv_done[T & 3]);
+          if (li == ntiles - 1) tc::commit(&sm->o_done);
+        }
+        __syncwarp();
+      }
+      ++done;
+    }
+    if (tc::elect_one()) {
+      tc::commit(&sm->pv_fin);
+      tc::mbar_drain(&sm->pv_fin, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    // An M = 64 accumulator occupies TMEM lanes 0-15 of each 32-lane quarter: a
+    // warp takes the 16 rows of its quarter and 32 heads, read with the 16x256b
+    // shape: lane t holds rows rq = t/4 and rq + 8 for heads 8c + 2cq + {0, 1}
+    // (c = 0..3, cq = t%4) of its half.
+    const int quarter = warp & 3, half = (warp - kSoftWarp0) >> 2;
+    const int rq = lane >> 2, cq = lane & 3;
+    const int rowA = quarter * 16 + rq, rowB = rowA + 8;  // tile rows of this thread
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    float *red = sm->red[quarter] + 32 * half;
+    // the 16-byte chunk of P^T that this lane names to stmatrix (128-byte rows, chunks swizzled by row & 7)
+    const int prow = quarter * 16 + (lane & 15);
+    const uint32_t pdst = tc::smem_u32(ps) + prow * 128 + (((4 * half + (lane >> 4)) ^ (prow & 7)) << 4);
+    const uint64_t scale2 = pack2(scale_log2, scale_log2);
+    bool ok = true;
+    uint32_t T = 0, done = 0;  // tiles so far, items with tiles so far
+    const int splits = gridDim.y, split = blockIdx.y;
+    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
+    const Item it = make_item(a, qv, raw, threadIdx.x == 32 * kSoftWarp0 && split == 0 ? a.status : nullptr);
+    raw = load_raw(a, qv + gridDim.x, qvs);
+    const int nh = min(kH, a.H - it.h0);
+    uint64_t nm[4], l[4];  // per pair of heads: minus the running maximum (of log2 logits), the running sum
+#pragma unroll
+    for (int c = 0; c < 4; ++c) nm[c] = pack2(-kFloor, -kFloor), l[c] = pack2(0.f, 0.f);
+    for (int li = 0; li < it.ntiles; ++li, ++T) {
+      const int buf = T & 1;
+      // (kv_full too: the row flags are the loaders' own writes)
+      bool got = tc::mbar_wait(&sm->kv_full[buf][0], (T >> 1) & 1, abort, a.status, lim);
+      got = got && tc::mbar_wait(&sm->s_full[buf], (T >> 1) & 1, abort, a.status, lim);
+      got = __all_sync(0xffffffffu, got);
+      tc::fence_after_sync();
+      const bool validA = sm->valid[buf][rowA], validB = sm->valid[buf][rowB];
+      const bool full = __all_sync(0xffffffffu, validA && validB);
+      uint32_t v[16];
+      tmem_ld_16x256b_x4(tmem + lane_off + kColS + 64 * buf + 32 * half, v);
+      tc::tmem_ld_wait();
+      // y = logit - running maximum, in log2 units; rows without a key are -inf
+      float2 yA[4], yB[4];
+      auto logits = [&](const uint64_t (&minus)[4]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          yA[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), scale2, minus[c]));
+          yB[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), scale2, minus[c]));
+        }
+        if (!full) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (!validA) yA[c] = make_float2(-INFINITY, -INFINITY);
+            if (!validB) yB[c] = make_float2(-INFINITY, -INFINITY);
+          }
+        }
+      };
+      logits(nm);
+      // The running maximum moves only when some logit of the tile exceeds it
+      // by more than 2^8 (always on the first row).
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) top = fmaxf(fmaxf(top, fmaxf(yA[c].x, yA[c].y)), fmaxf(yB[c].x, yB[c].y));
+      bool rescale = false;
+      if (bar_any(1 + half, 128, top > kRescaleLog2 || !(got && ok))) {
+        if (bar_any(1 + half, 128, !(got && ok))) {  // S^T(li) missing, or the previous P.V never completed
+          ok = false;
+          break;
+        }
+        // per-head tile maximum: over the thread's two rows, then over the 8
+        // lanes of the same cq, then over the 4 warps
+        const uint64_t zero[4] = {0, 0, 0, 0};
+        logits(zero);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float2 mx = make_float2(fmaxf(yA[c].x, yB[c].x), fmaxf(yA[c].y, yB[c].y));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+            mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+          }
+          if (rq == 0) *reinterpret_cast<float2 *>(red + 8 * c + 2 * cq) = mx;
+        }
+        named_sync(1 + half, 128);
+        if (quarter == 0) {
+          const int h = 32 * half + lane;
+          const float tm = fmaxf(fmaxf(sm->red[0][h], sm->red[1][h]), fmaxf(sm->red[2][h], sm->red[3][h]));
+          const float mo = sm->mref[h];
+          const bool up = tm > mo + kRescaleLog2;
+          if (up) sm->mref[h] = tm;
+          sm->alpha[h] = up ? exp2f(mo - tm) : 1.f;
+          const bool any = __any_sync(0xffffffffu, up && mo != kFloor);
+          if (lane == 0) sm->rescale[half] = any ? 1 : 0;
+        }
+        named_sync(1 + half, 128);
+        rescale = sm->rescale[half] != 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 m = *reinterpret_cast<const float2 *>(&sm->mref[32 * half + 8 * c + 2 * cq]);
+          nm[c] = pack2(-m.x, -m.y);
+          if (rescale) {
+            const float2 al = *reinterpret_cast<const float2 *>(&sm->alpha[32 * half + 8 * c + 2 * cq]);
+            l[c] = fma2(l[c], pack2(al.x, al.y), 0);
+          }
+        }
+        logits(nm);
+      }
+      // P = 2^y, rounded to bf16 and summed per head. The sums take the same
+      // bf16 weights as P.V, so that a dominant row's weight (up to 2^8 between
+      // rescales) cancels exactly.
+      uint32_t pA[4], pB[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const __nv_bfloat162 ta = __floats2bfloat162_rn(ex2_approx(yA[c].x), ex2_approx(yA[c].y));
+        const __nv_bfloat162 tb = __floats2bfloat162_rn(ex2_approx(yB[c].x), ex2_approx(yB[c].y));
+        pA[c] = *reinterpret_cast<const uint32_t *>(&ta);
+        pB[c] = *reinterpret_cast<const uint32_t *>(&tb);
+        l[c] = add2(l[c], pack2(__uint_as_float(pA[c] << 16), __uint_as_float(pA[c] & 0xffff0000u)));
+        l[c] = add2(l[c], pack2(__uint_as_float(pB[c] << 16), __uint_as_float(pB[c] & 0xffff0000u)));
+      }
+      // P.V of the tile before has to be complete before P^T, and where the
+      // maximum moved O^T too, are written again.
+      if (T > 0) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->pv_done[(T - 1) & 3], ((T - 1) >> 2) & 1, abort, a.status, lim));
+        tc::fence_after_sync();
+      }
+      stmatrix_x4(pdst, pA[0], pB[0], pA[1], pB[1]);
+      stmatrix_x4(pdst ^ 32, pA[2], pB[2], pA[3], pB[3]);
+      if (li > 0 && rescale) {
+        if (ok) {
+#pragma unroll 1
+          for (int m = 0; m < NB; ++m) {  // 16 heads of a 128-dim chunk at a time
+            const int h = 32 * half + 16 * (m & 1);
+            uint32_t o[16];
+            const uint32_t ta = tmem + lane_off + 64 * (m >> 1) + h;
+            tmem_ld16(ta, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * sm->alpha[h + c]);
+            tmem_st16(ta, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tc::fence_before_sync();
+      tc::mbar_arrive(&sm->p_full);
+    }
+    // Per-head sums, and what the output is multiplied by.
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float2 s = unpack2(l[c]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+      }
+      if (rq == 0) *reinterpret_cast<float2 *>(red + 8 * c + 2 * cq) = s;
+    }
+    named_sync(1 + half, 128);
+    if (quarter == 0) {
+      const int h = 32 * half + lane;
+      const float ls = (sm->red[0][h] + sm->red[1][h]) + (sm->red[2][h] + sm->red[3][h]);
+      const float mr = sm->mref[h];
+      if (h < nh) {
+        if (splits > 1) {
+          reinterpret_cast<float2 *>(a.part_ml)[((size_t)it.qq * a.H + it.h0 + h) * splits + split] = make_float2(mr, ls);
+        } else {  // fold in the sink (logit sink[h], value 0) and normalise
+          const float sk = a.sink[it.h0 + h] * kLog2e, M = fmaxf(mr, sk), wm = exp2f(mr - M);
+          const float Ls = ls * wm + exp2f(sk - M);
+          sm->norm[h] = Ls == 0.f ? 0.f : wm / Ls;
+        }
+      }
+      sm->mref[h] = kFloor;  // for the next item, which reads it after a barrier
+      if (it.ntiles > 0) tc::mbar_arrive(&sm->norm_full);
+    }
+    named_sync(1 + half, 128);
+    // These warps' half of the output (all of it where the item has no tiles).
+    const bool some = it.ntiles > 0;
+    if (some) {
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm->o_done, done & 1, abort, a.status, lim));
+      tc::fence_after_sync();
+      ++done;
+    }
+    if (!ok) break;
+    write_out<NB>(a, tmem + 32 * half, sm->norm + 32 * half, (size_t)it.qq * a.H + it.h0 + 32 * half, nh - 32 * half, quarter, 0,
+                  some ? NB / 2 : NB, some, &sm->o_free);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kPvWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+bool aligned(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+template <int NB, bool kInt4>
+cudaError_t launch_nb(const PagedMqaArgs &a, const CUtensorMap &tm_q, int splits, cudaStream_t stream) {
+  static DeviceOnce attr;
+  once_per_device(attr, [] {
+    cudaFuncSetAttribute(paged_mqa_tc_kernel<NB, kInt4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(NB));
+  });
+  const int groups = (a.H + kH - 1) / kH;
+  const long long qvs = (long long)a.Q * groups;
+  const int sms = device_sm_count();
+  if (qvs > 0x7fffffffLL - sms) return cudaErrorInvalidValue;  // (item numbers pass the last by a grid)
+  const long long most = sms / splits > 0 ? sms / splits : 1;
+  return launch_pdl(paged_mqa_tc_kernel<NB, kInt4>, dim3((unsigned)(qvs < most ? qvs : most), splits), dim3(kThreads),
+                    smem_bytes(NB), stream, tm_q, a, (int)qvs, a.scale * kLog2e);
+}
+
+}  // namespace
+
+int paged_mqa_tc_splits(int Q, int H, int D, int rows_max) {
+  if (D % 128 || D > 512) return 0;
+  const int tiles = (rows_max + 2 * kRows - 1) / kRows;  // (the window's padding to whole tiles)
+  const long long qv = (long long)Q * ((H + kH - 1) / kH);
+  long long s = device_sm_count() / qv;
+  if (s > tiles) s = tiles;
+  return (int)(s < 1 ? 1 : s > kPagedMaxSplits ? kPagedMaxSplits : s);
+}
+
+cudaError_t launch_paged_mqa_tc(const PagedMqaArgs &args, void *partials, cudaStream_t stream, bool *taken) {
+  *taken = false;
+  PagedMqaArgs a = args;
+  const int D = a.cache.D;
+  const bool int4 = a.cache.scales != nullptr;
+  if (a.dtype != CSA_DTYPE_BF16 || D % 128 || D > 512 || !aligned(a.q, 16) || !aligned(a.kv_win, 16) ||
+      !aligned(a.out, 16))
+    return cudaSuccess;
+  if (!aligned(a.cache.pages, 16) || !aligned(a.cache.scales, 16)) return cudaSuccess;
+  CUtensorMap tm_q;
+  if (!make_tmap_bf16_3d(&tm_q, a.q, D, a.H, a.Q, 64, kH)) return cudaSuccess;
+  const int splits = paged_mqa_tc_splits(a.Q, a.H, D, a.rows_max);
+  paged_mqa_carve(a, partials, splits);
+  *taken = true;
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (2 * (D / 128) + int4) {
+    case 2: e = launch_nb<2, false>(a, tm_q, splits, stream); break;
+    case 3: e = launch_nb<2, true>(a, tm_q, splits, stream); break;
+    case 4: e = launch_nb<4, false>(a, tm_q, splits, stream); break;
+    case 5: e = launch_nb<4, true>(a, tm_q, splits, stream); break;
+    case 6: e = launch_nb<6, false>(a, tm_q, splits, stream); break;
+    case 7: e = launch_nb<6, true>(a, tm_q, splits, stream); break;
+    case 8: e = launch_nb<8, false>(a, tm_q, splits, stream); break;
+    case 9: e = launch_nb<8, true>(a, tm_q, splits, stream); break;
+  }
+  return e == cudaSuccess && splits > 1 ? launch_paged_merge(a, splits, stream) : e;
+}
+
+}  // namespace csa

@@ -43,6 +43,21 @@ inline bool make_tmap_bf16_2d(CUtensorMap *m, const void *base, uint64_t inner, 
   return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, row_bytes, box_inner, box_outer);
 }
 
+// Dense 3-D bf16 tensor [outer][mid][inner], boxes of box_inner x box_mid x 1.
+inline bool make_tmap_bf16_3d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t mid, uint64_t outer,
+                              uint32_t box_inner, uint32_t box_mid) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {inner, mid, outer};
+  cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
+  cuuint32_t box[3] = {box_inner, box_mid, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // One-byte elements (FP8 codes moved as raw bytes).
 inline bool make_tmap_u8_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                             uint32_t box_inner, uint32_t box_outer) {
