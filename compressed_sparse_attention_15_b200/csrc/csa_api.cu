@@ -2,6 +2,7 @@
 // workspace carving and dispatch to the kernels. Nothing here allocates,
 // frees or synchronises (except csa_workspace_status, which is documented to
 // synchronise).
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -446,7 +447,11 @@ static int paged_rows(const void *rows, long long row_stride, long long seq_stri
   a.dtype = dtype;
   a.rope_dims = rope_dims;
   a.pos_stride = pos_stride;
-  a.rope_theta = rope_theta;
+  if (rope_dims) {
+    const long double l = log2l((long double)rope_theta);
+    a.log2_theta[0] = (double)l;
+    a.log2_theta[1] = (double)(l - (long double)a.log2_theta[0]);
+  }
   a.pos0 = pos0;
   a.status = status_of(ws);
   return cuda_rc(launch_paged_rows(a, append, stream));

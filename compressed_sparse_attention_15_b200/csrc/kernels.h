@@ -233,7 +233,7 @@ struct PagedRowsArgs {
   long long row_stride, seq_stride;  // of rows, in elements
   int B, n, dtype;
   int rope_dims, pos_stride;
-  double rope_theta;
+  double log2_theta[2];      // of the rotation's base, as a double and the rest of it
   const int64_t *pos0;
   uint32_t *status;
 };

@@ -44,12 +44,29 @@ __device__ __forceinline__ float e4m3_value(uint8_t u) {
   return float(t);
 }
 
-// The 8 dims of a word under scale s.
+__device__ __forceinline__ uint32_t bf16x2_dup(float x) {
+  const __nv_bfloat162 t = __float2bfloat162_rn(x);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
+
+// The 8 dims of a word as 4 pairs of bf16, exactly: a nibble c placed in the
+// mantissa of 128 is 128 + c, and one packed fused multiply-add makes
+// (128 + c) s - 136 s = (c - 8) s of it. sc and off hold s and -136 s (17 times
+// 8 to 15 eighths: 8 significant bits), twice each.
+__device__ __forceinline__ void widen8(uint32_t w, uint32_t sc, uint32_t off, uint32_t (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[k]) : "r"(((w >> (4 * k)) & 0x000f000fu) | 0x43004300u), "r"(sc), "r"(off));
+}
+
+// The same in fp32.
 __device__ __forceinline__ void unpack8(uint32_t w, float s, float (&v)[8]) {
+  uint32_t t[4];
+  widen8(w, bf16x2_dup(s), bf16x2_dup(-136.f * s), t);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * s;
-    v[2 * i + 1] = (float)((int)((w >> (4 * i + 16)) & 15u) - 8) * s;
+    v[2 * i] = __uint_as_float(t[i] << 16);
+    v[2 * i + 1] = __uint_as_float(t[i] & 0xffff0000u);
   }
 }
 

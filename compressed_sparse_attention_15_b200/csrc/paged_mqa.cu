@@ -214,59 +214,88 @@ __global__ void __launch_bounds__(kThreads) paged_mqa_kernel(PagedMqaArgs a, int
 // Merge of a (query, head)'s splits with its sink:
 //   M = max(max_s m_s, sink), L = sum_s l_s 2^(m_s - M) + 2^(sink - M),
 //   out = sum_s O_s 2^(m_s - M) / L.
-// One block per (query, head); its bytes are the partials', just written, so L2 serves them.
-template <typename T>
+// A block takes 512 dims, four a thread, and each thread every split; or (kFew,
+// where that leaves few blocks) 128 dims, and warp w the splits w, w + 4, ... Its
+// bytes are the partials', just written, so L2 serves them; the first of them
+// are on their way while the weights are formed.
+template <typename T, bool kVec, bool kFew>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const float *part_o, const float *part_ml, const float *sink,
                                                           T *out, int H, int D, int splits) {
-  __shared__ float w[kPagedMaxSplits];
-  __shared__ float inv;
+  __shared__ float4 acc_s[kFew ? 4 : 1][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kStep = kFew ? 4 : 1;
+  const size_t qh = blockIdx.x;
+  const int d0 = (kFew ? 128 : 512) * blockIdx.y, d = d0 + 4 * (kFew ? lane : (int)threadIdx.x);
+  const int s0 = kFew ? warp : 0;
   pdl_wait();
   pdl_release();
-  const size_t qh = blockIdx.x;
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    const float2 *ml = reinterpret_cast<const float2 *>(part_ml) + qh * splits;
-    const float sk = sink[qh % H] * kLog2e;
-    float M = sk;
-    for (int s = lane; s < splits; s += 32) M = fmaxf(M, ml[s].x);
-    M = warp_max(M);
-    float L = 0.f;
-    for (int s = lane; s < splits; s += 32) {
-      const float2 v = ml[s];
-      const float c = exp2f(v.x - M);
-      w[s] = c;
-      L = fmaf(v.y, c, L);
+  const float *src = part_o + qh * splits * D + d;
+  auto load = [&](int s) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s >= splits) return v;
+    const float *p = src + (size_t)s * D;
+    if (kVec) {
+      if (d < D) v = __ldcg(reinterpret_cast<const float4 *>(p));
+    } else {
+      if (d < D) v.x = __ldcg(p);
+      if (d + 1 < D) v.y = __ldcg(p + 1);
+      if (d + 2 < D) v.z = __ldcg(p + 2);
+      if (d + 3 < D) v.w = __ldcg(p + 3);
     }
-    L = warp_sum(L) + exp2f(sk - M);
-    if (lane == 0) inv = L == 0.f ? 0.f : 1.f / L;
-  }
-  __syncthreads();
-  const float *src = part_o + qh * splits * D;
-  if (D % 4 == 0) {
-    for (int d = 4 * threadIdx.x; d < D; d += 512) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int s = 0; s < splits; ++s) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)s * D + d));
-        const float c = w[s];
-        acc.x = fmaf(c, v.x, acc.x);
-        acc.y = fmaf(c, v.y, acc.y);
-        acc.z = fmaf(c, v.z, acc.z);
-        acc.w = fmaf(c, v.w, acc.w);
+    return v;
+  };
+  constexpr int kAhead = 4;
+  float4 v[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) v[i] = load(s0 + kStep * i);
+  const float2 *ml = reinterpret_cast<const float2 *>(part_ml) + qh * splits;
+  const float sk = sink[qh % H] * kLog2e;
+  float M = sk, L = 0.f;
+  for (int s = lane; s < splits; s += 32) M = fmaxf(M, ml[s].x);
+  M = warp_max(M);
+  for (int s = lane; s < splits; s += 32) L = fmaf(ml[s].y, exp2f(ml[s].x - M), L);
+  L = warp_sum(L) + exp2f(sk - M);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = s0; s < splits; s += kStep * kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s + kStep * i < splits) {
+        const float c = exp2f(ml[s + kStep * i].x - M);
+        acc.x = fmaf(c, v[i].x, acc.x);
+        acc.y = fmaf(c, v[i].y, acc.y);
+        acc.z = fmaf(c, v[i].z, acc.z);
+        acc.w = fmaf(c, v[i].w, acc.w);
+        v[i] = load(s + kStep * (i + kAhead));
       }
-      T *o = out + qh * D + d;
-      o[0] = from_f<T>(acc.x * inv);
-      o[1] = from_f<T>(acc.y * inv);
-      o[2] = from_f<T>(acc.z * inv);
-      o[3] = from_f<T>(acc.w * inv);
+    }
+  }
+  if constexpr (kFew) {
+    acc_s[warp][lane] = acc;
+    __syncthreads();
+    if (d0 + (int)threadIdx.x < D) {
+      const float *a = reinterpret_cast<const float *>(acc_s) + threadIdx.x;
+      out[qh * D + d0 + threadIdx.x] = from_f<T>(((a[0] + a[128]) + (a[256] + a[384])) * inv);
     }
   } else {
-    for (int d = threadIdx.x; d < D; d += 128) {
-      float acc = 0.f;
-      for (int s = 0; s < splits; ++s) acc = fmaf(w[s], __ldcg(src + (size_t)s * D + d), acc);
-      out[qh * D + d] = from_f<T>(acc * inv);
-    }
+    const float o[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (d + e < D) out[qh * D + d + e] = from_f<T>(o[e] * inv);
   }
+}
+
+template <typename T>
+cudaError_t launch_merge(const PagedMqaArgs &a, int splits, cudaStream_t stream) {
+  const long long blocks = (long long)a.Q * a.H;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int D = a.cache.D;
+  const bool few = blocks < 4 * device_sm_count();
+  auto kern = D % 4 ? (few ? paged_merge_kernel<T, false, true> : paged_merge_kernel<T, false, false>)
+                    : (few ? paged_merge_kernel<T, true, true> : paged_merge_kernel<T, true, false>);
+  const int dims = few ? 128 : 512;
+  return launch_pdl(kern, dim3((unsigned)blocks, (D + dims - 1) / dims), dim3(128), 0, stream, (const float *)a.part_o,
+                    (const float *)a.part_ml, a.sink, static_cast<T *>(a.out), a.H, D, splits);
 }
 
 int heads_per_block(int H) { return H >= 5 ? 8 : H >= 3 ? 4 : H; }
@@ -318,13 +347,7 @@ size_t partial_floats(int Q, int H, int D, int splits) {
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedMqaArgs &a, int splits, cudaStream_t stream) {
-  const long long blocks = (long long)a.Q * a.H;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (a.dtype == CSA_DTYPE_F32)
-    return launch_pdl(paged_merge_kernel<float>, dim3((unsigned)blocks), dim3(128), 0, stream, (const float *)a.part_o,
-                      (const float *)a.part_ml, a.sink, static_cast<float *>(a.out), a.H, a.cache.D, splits);
-  return launch_pdl(paged_merge_kernel<bf16>, dim3((unsigned)blocks), dim3(128), 0, stream, (const float *)a.part_o,
-                    (const float *)a.part_ml, a.sink, static_cast<bf16 *>(a.out), a.H, a.cache.D, splits);
+  return a.dtype == CSA_DTYPE_F32 ? launch_merge<float>(a, splits, stream) : launch_merge<bf16>(a, splits, stream);
 }
 
 size_t paged_mqa_partial_bytes(int Q, int H, int D, int rows_max) {

@@ -8,10 +8,8 @@
 // and so are the online softmax (running maximum moved only when a logit passes
 // it by 2^8), the two tile buffers, and the issue order.
 //
-// A tile of 4-bit rows is widened to bf16 on its way into shared memory. One
-// packed fused multiply-add makes two values, exactly: a nibble c placed in the
-// mantissa of 128 is 128 + c, and (128 + c) s - 136 s = (c - 8) s, where s, 136 s
-// (17 times 8 to 15 eighths: 8 significant bits) and the result are bf16 numbers. A lane takes 32 bytes of a row, the 64 dims of one
+// A tile of 4-bit rows is widened to bf16 (exactly, two dims an instruction:
+// widen8) on its way into shared memory. A lane takes 32 bytes of a row, the 64 dims of one
 // 128-byte swizzled line, and 8 lanes take 8 rows, so that every 16-byte store
 // of theirs falls into distinct banks. The packed rows come through a staging
 // tile, which two warps fill by asynchronous copies while the tile before is
@@ -257,17 +255,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t bf16x2_dup(float x) {
-  const __nv_bfloat162 t = __float2bfloat162_rn(x);
-  return *reinterpret_cast<const uint32_t *>(&t);
-}
-
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -296,10 +283,8 @@ __device__ __forceinline__ void store_widened(const Packed &u, uint32_t chunk0) 
   }
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const uint32_t w = u.w[c];
     uint32_t v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = fma_bf16x2(((w >> (4 * k)) & 0x000f000fu) | 0x43004300u, sc[c >> 1], off[c >> 1]);
+    widen8(u.w[c], sc[c >> 1], off[c >> 1], v);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk0 ^ (c << 4)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                  : "memory");
   }
@@ -918,8 +903,10 @@ int paged_mqa_tc_splits(int Q, int H, int D, int rows_max) {
   if (D % 128 || D > 512) return 0;
   const int tiles = (rows_max + 2 * kRows - 1) / kRows;  // (the window's padding to whole tiles)
   const long long qv = (long long)Q * ((H + kH - 1) / kH);
+  // a block per SM, and no split below two tiles: a split of one tile writes and has merged as many bytes of
+  // partials as two, for half of the work
   long long s = device_sm_count() / qv;
-  if (s > tiles) s = tiles;
+  if (s > tiles / 2) s = tiles / 2;
   return (int)(s < 1 ? 1 : s > kPagedMaxSplits ? kPagedMaxSplits : s);
 }
 

@@ -7,14 +7,12 @@ arithmetic of the method. Names follow the C entry points.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
 from . import _lib
 
-_HERE = contextlib.nullcontext()
 _DT = {torch.float32: _lib.CSA_DTYPE_F32, torch.bfloat16: _lib.CSA_DTYPE_BF16}
 
 
@@ -188,12 +186,40 @@ def hadamard_rows(x, fp8: bool = False):
 
 
 # ------------------------------------------------------- norm of the activations
+# The calls from here on are short next to a Python call: their checks take one
+# look at each tensor, and pointers go to the library as plain integers.
 
-def _on(t: torch.Tensor):
-    """A context in which t's device is the current one (the library launches
-    on the current device)."""
-    i = t.device.index
-    return _HERE if i is None or i == torch.cuda.current_device() else torch.cuda.device(i)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _check(t, name: str, dtype, dev: int, contiguous: bool = True):
+    """_need for a tensor of a dtype on CUDA device number dev."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev >= 0 and t.dtype is dtype and (
+            not contiguous or t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtype=dtype, device=None if dev < 0 else torch.device("cuda", dev), contiguous=contiguous)
+    return t.data_ptr()
+
+
+def _call(name: str, dev: int, *args):
+    """The C entry point on device number dev and its current stream (the last argument)."""
+    fn = getattr(_lib.lib(), name)
+    if _current_device() == dev:
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
+    if rc:
+        _lib.check(name, rc)
+
+
+def _workspace(ws, device, dev: int, nbytes: int = 256):
+    """(pointer, size) of a workspace on device number dev."""
+    w = (ws or Workspace(device)).get(nbytes)
+    if w.get_device() != dev:
+        raise ValueError(f"ws is on {w.device}, expected {device}")
+    return w.data_ptr(), w.numel()
 
 
 def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, fp8: bool = False, group: int = 0, out=None,
@@ -206,52 +232,49 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, fp8: bool = False, 
     [..., D / group]), followed with a residual by h = x + residual (sum_out,
     which may be residual itself)."""
     _need(x, "x", contiguous=False)
-    dev = x.device
-    if x.dim() < 1 or x.numel() and x.stride(-1) != 1:
-        raise ValueError("x must be [..., D] with contiguous rows")
-    D = x.shape[-1]
-    _need(weight, "weight", dtype=torch.float32, device=dev)
-    if weight.shape != (D,):
-        raise ValueError("weight must be [D]")
-    if x.is_contiguous():
+    dev, dtype, shape, code = x.get_device(), x.dtype, x.shape, _dtype_code(x)
+    D = shape[-1] if shape else 0
+    if x.is_contiguous() and shape:
         stride = 0
-    elif x.dim() == 2 and x.stride(0) >= D:
+    elif len(shape) == 2 and x.stride(1) == 1 and x.stride(0) >= D:
         stride = x.stride(0)
     else:
-        raise ValueError("x must be contiguous, or [rows, D] with rows at least D apart")
+        raise ValueError("x must be contiguous, or [rows, D] with contiguous rows at least D apart")
+    w = _check(weight, "weight", torch.float32, dev)
+    if weight.shape != (D,):
+        raise ValueError("weight must be [D]")
+    res = total = scales = None
     if residual is not None:
-        _need(residual, "residual", dtype=x.dtype, device=dev)
+        res = _check(residual, "residual", dtype, dev)
         if sum_out is None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _need(sum_out, "sum_out", dtype=x.dtype, device=dev)
-        if residual.shape != x.shape or sum_out.shape != x.shape:
+            sum_out = torch.empty_like(residual)
+        total = _check(sum_out, "sum_out", dtype, dev)
+        if residual.shape != shape or sum_out.shape != shape:
             raise ValueError("residual and sum_out must have x's shape")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    rows = x.numel() // D if D else 0
+    out_dtype = torch.uint8 if fp8 else dtype
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.uint8 if fp8 else x.dtype, device=dev)
-    _need(out, "out", dtype=torch.uint8 if fp8 else x.dtype, device=dev)
-    if out.shape != x.shape:
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    y = _check(out, "out", out_dtype, dev)
+    if out.shape != shape:
         raise ValueError("out must have x's shape")
     if fp8:
-        if group and D % group:
+        if group < 0 or group and D % group:
             raise ValueError("group must divide D")
+        want = (*shape[:-1], D // (group or D) if D else 0)
         if out_scales is None:
-            out_scales = torch.empty((*x.shape[:-1], D // (group or D)), dtype=torch.float32, device=dev)
-        _need(out_scales, "out_scales", dtype=torch.float32, device=dev)
-        if out_scales.shape != (*x.shape[:-1], D // (group or D)):
+            out_scales = torch.empty(want, dtype=torch.float32, device=x.device)
+        scales = _check(out_scales, "out_scales", torch.float32, dev)
+        if out_scales.shape != want:
             raise ValueError("out_scales must be [..., D / group]")
     elif out_scales is not None or group:
         raise ValueError("out_scales and group are for fp8 output")
-    code = _dtype_code(x)
-    with _on(x):
-        rc = _lib.lib().csa_add_rmsnorm(_ptr(x), stride, _ptr(residual), _ptr(weight), float(eps), _ptr(out),
-                                        _ptr(out_scales), _ptr(sum_out), rows, D, int(group), code,
-                                        _lib.CSA_DTYPE_E4M3 if fp8 else code, _stream(dev))
-    _lib.check("csa_add_rmsnorm", rc)
-    y = (out, out_scales) if fp8 else (out,)
-    return y if residual is None else (*y, sum_out)
+    _call("csa_add_rmsnorm", dev, x.data_ptr(), stride, res, w, float(eps), y, scales, total, x.numel() // D if D else 0,
+          D, int(group), code, _lib.CSA_DTYPE_E4M3 if fp8 else code)
+    if residual is None:
+        return (out, out_scales) if fp8 else (out,)
+    return (out, out_scales, sum_out) if fp8 else (out, sum_out)
 
 
 # ------------------------------------------------------------- A2 + A3
@@ -450,34 +473,35 @@ def hca_mqa(q, kv_cmp, n_cmp, kv_win, win_end, sink, scale: float, win_len: int,
 # ------------------------------------------------------- paged cache
 
 def _paged(pages, scales, page_table, dtype, dev):
-    """Checks a paged cache; returns (D, num_pages, page_size, B, pages_per_seq, cache_dtype)."""
-    _need(pages, "pages", device=dev)
-    _need(page_table, "page_table", dtype=torch.int32, device=dev)
+    """Checks a paged cache on device number dev; returns its pointers (pages, scales, table)
+    and (D, num_pages, page_size, B, pages_per_seq, cache_dtype)."""
+    t = _check(page_table, "page_table", torch.int32, dev)
+    if scales is None:
+        p, s = _check(pages, "pages (without scales)", dtype, dev), None
+        cache = _DT[dtype]
+    else:
+        p = _check(pages, "pages (with scales)", torch.uint8, dev)
+        kind = getattr(scales, "dtype", None)
+        if kind is not torch.uint8 and kind is not torch.float8_e4m3fn:
+            raise TypeError("scales must be E4M3 (or its bytes as uint8)")
+        s = _check(scales, "scales", kind, dev)
+        cache = _lib.CSA_CACHE_INT4
     if pages.dim() != 3 or page_table.dim() != 2:
         raise ValueError("pages must be [num_pages, page_size, D] (D / 2 bytes in 4 bits), page_table [B, pages_per_seq]")
     num_pages, page_size, D = pages.shape
-    if scales is None:
-        if pages.dtype != dtype:
-            raise TypeError(f"pages must be {dtype}, or uint8 codes with scales")
-        cache = _DT.get(dtype, -1)
-    else:
-        _need(pages, "pages", dtype=torch.uint8)
-        if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.uint8, torch.float8_e4m3fn):
-            raise TypeError("scales must be E4M3 (or its bytes as uint8)")
-        _need(scales, "scales", device=dev)
+    if scales is not None:
         D *= 2
         if D % 16 or scales.shape != (num_pages, page_size, D // 16):
             raise ValueError("scales must be [num_pages, page_size, D / 16] with D a multiple of 16")
-        cache = _lib.CSA_CACHE_INT4
-    return D, num_pages, page_size, *page_table.shape, cache
+    B, per = page_table.shape
+    return (p, s, t), (D, num_pages, page_size, B, per, cache)
 
 
-def _paged_counts(entry0, n_new, B, dev):
-    for t, nm in ((entry0, "entry0"), (n_new, "n_new")):
-        if t is not None or nm == "entry0":
-            _need(t, nm, dtype=torch.int32, device=dev)
-            if t.shape != (B,):
-                raise ValueError(f"{nm} must be [B]")
+def _per_sequence(t, name, dtype, B, dev):
+    p = _check(t, name, dtype, dev)
+    if t.shape != (B,):
+        raise ValueError(f"{name} must be [B]")
+    return p
 
 
 def paged_append(kv, pages, scales, page_table, entry0, n_new=None, rope=None, ws: Workspace | None = None):
@@ -491,27 +515,24 @@ def paged_append(kv, pages, scales, page_table, entry0, n_new=None, rope=None, w
     each row's last rope_dims dims for position pos0[b] + i * pos_stride.
     Returns pages."""
     _need(kv, "kv", contiguous=False)
-    dev, code = kv.device, _dtype_code(kv)
-    D, num_pages, page_size, B, per, cache = _paged(pages, scales, page_table, kv.dtype, dev)
-    if kv.dim() != 3 or kv.shape[0] != B or kv.shape[2] != D:
+    dev, code = kv.get_device(), _dtype_code(kv)
+    (p, s, t), (D, num_pages, page_size, B, per, cache) = _paged(pages, scales, page_table, kv.dtype, dev)
+    shape = kv.shape
+    if len(shape) != 3 or shape[0] != B or shape[2] != D:
         raise ValueError("kv must be [B, n, D]")
-    n = kv.shape[1]
-    rs, ss = (kv.stride(1) if n > 1 else D), (kv.stride(0) if B > 1 else 0)
-    if kv.numel() and (kv.stride(2) != 1 and D > 1 or rs < D or B > 1 and ss < 1):
-        raise ValueError("kv must have contiguous rows, at least D apart, and a positive sequence stride")
-    _paged_counts(entry0, n_new, B, dev)
+    n = shape[1]
+    rs = ss = 0
+    if not kv.is_contiguous():
+        ss, rs, one = kv.stride()
+        if D > 1 and one != 1 or n > 1 and rs < D or B > 1 and ss < 1:
+            raise ValueError("kv must have contiguous rows, at least D apart, and a positive sequence stride")
+        rs, ss = (rs if n > 1 else 0), (ss if B > 1 else 0)
+    e0 = _per_sequence(entry0, "entry0", torch.int32, B, dev)
+    nn = None if n_new is None else _per_sequence(n_new, "n_new", torch.int32, B, dev)
     rope_dims, theta, pos0, pos_stride = rope or (0, 0.0, None, 0)
-    if pos0 is not None:
-        _need(pos0, "pos0", dtype=torch.int64, device=dev)
-        if pos0.shape != (B,):
-            raise ValueError("pos0 must be [B]")
-    with _on(kv):
-        w = (ws or Workspace(dev)).get(256)
-        rc = _lib.lib().csa_paged_append(
-            _ptr(kv), max(rs, 0), max(ss, 0), _ptr(pages), _ptr(scales), _ptr(page_table), _ptr(entry0), _ptr(n_new), B, n,
-            D, num_pages, page_size, per, int(rope_dims), float(theta), _ptr(pos0), int(pos_stride), code, cache, _ptr(w),
-            w.numel(), _stream(dev))
-    _lib.check("csa_paged_append", rc)
+    pos = None if pos0 is None else _per_sequence(pos0, "pos0", torch.int64, B, dev)
+    _call("csa_paged_append", dev, kv.data_ptr(), rs, ss, p, s, t, e0, nn, B, n, D, num_pages, page_size, per, int(rope_dims),
+          float(theta), pos, int(pos_stride), code, cache, *_workspace(ws, kv.device, dev))
     return pages
 
 
@@ -521,43 +542,51 @@ def paged_read(pages, scales, page_table, entry0, n: int, n_new=None, out=None, 
     were in ``out`` (zero when allocated here, in ``dtype``: bf16 by default
     for a 4-bit cache). out: rows contiguous, any sequence stride."""
     _need(pages, "pages")
-    dev = pages.device
+    dev, n = pages.get_device(), int(n)
     if out is not None:
-        _need(out, "out", device=dev, contiguous=False)
+        _need(out, "out", device=pages.device, contiguous=False)
         dtype = out.dtype
     elif dtype is None:
         dtype = torch.bfloat16 if scales is not None else pages.dtype
-    D, num_pages, page_size, B, per, cache = _paged(pages, scales, page_table, dtype, dev)
+    code = _DT.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; use torch.float32 or torch.bfloat16")
+    (p, s, t), (D, num_pages, page_size, B, per, cache) = _paged(pages, scales, page_table, dtype, dev)
+    ss = 0
     if out is None:
-        out = torch.zeros((B, int(n), D), dtype=dtype, device=dev)
-    if out.shape != (B, n, D) or out.numel() and (D > 1 and out.stride(2) != 1 or n > 1 and out.stride(1) != D):
-        raise ValueError("out must be [B, n, D] with contiguous [n, D] rows")
-    _paged_counts(entry0, n_new, B, dev)
-    with _on(pages):
-        w = (ws or Workspace(dev)).get(256)
-        rc = _lib.lib().csa_paged_read(
-            _ptr(pages), _ptr(scales), _ptr(page_table), _ptr(entry0), _ptr(n_new), _ptr(out),
-            out.stride(0) if B > 1 else 0, B, int(n), D, num_pages, page_size, per, _dtype_code(out), cache, _ptr(w),
-            w.numel(), _stream(dev))
-    _lib.check("csa_paged_read", rc)
+        out = torch.zeros((B, n, D), dtype=dtype, device=pages.device)
+    elif out.shape != (B, n, D):
+        raise ValueError("out must be [B, n, D]")
+    elif not out.is_contiguous():
+        if D > 1 and out.stride(2) != 1 or n > 1 and out.stride(1) != D:
+            raise ValueError("out must have contiguous [n, D] rows")
+        ss = out.stride(0) if B > 1 else 0
+        if B > 1 and ss < n * D:
+            raise ValueError("out's sequences must not overlap")
+    e0 = _per_sequence(entry0, "entry0", torch.int32, B, dev)
+    nn = None if n_new is None else _per_sequence(n_new, "n_new", torch.int32, B, dev)
+    _call("csa_paged_read", dev, p, s, t, e0, nn, out.data_ptr(), ss, B, n, D, num_pages, page_size, per, code, cache,
+          *_workspace(ws, pages.device, dev))
     return out
 
 
 def _paged_mqa(name, q, pages, scales, page_table, rows, kv_win, win_end, sink, scale, win_len, q_per_seq, out, ws):
     _need(q, "q")
-    dev, code = q.device, _dtype_code(q)
-    if q.dim() != 3:
+    dev, code, dtype, shape = q.get_device(), _dtype_code(q), q.dtype, q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [Q, H, D]")
-    Q, H, D = q.shape
-    D2, num_pages, page_size, B, per, cache = _paged(pages, scales, page_table, q.dtype, dev)
-    _need(sink, "sink", dtype=torch.float32, device=dev)
-    _need(rows, "idx" if name == "csa_paged_sparse_mqa" else "n_cmp", dtype=torch.int32, device=dev)
-    if D2 != D or sink.shape != (H,) or rows.shape[:1] != (Q,):
+    Q, H, D = shape
+    (p, s, t), (D2, num_pages, page_size, B, per, cache) = _paged(pages, scales, page_table, dtype, dev)
+    sk = _check(sink, "sink", torch.float32, dev)
+    sparse = name == "csa_paged_sparse_mqa"
+    r = _check(rows, "idx" if sparse else "n_cmp", torch.int32, dev)
+    if rows.dim() != (2 if sparse else 1):
+        raise ValueError("idx must be [Q, k]" if sparse else "n_cmp must be [Q]")
+    if D2 != D or sink.shape != (H,) or rows.shape[0] != Q:
         raise ValueError("shape mismatch among q [Q,H,D], pages [P,page,D], sink [H], idx [Q,k] or n_cmp [Q]")
-    T_raw = 0
+    T_raw, win, end, win_len = 0, None, None, int(win_len)
     if win_len:
-        _need(kv_win, "kv_win", dtype=q.dtype, device=dev)
-        _need(win_end, "win_end", dtype=torch.int32, device=dev)
+        win, end = _check(kv_win, "kv_win", dtype, dev), _check(win_end, "win_end", torch.int32, dev)
         if kv_win.dim() != 3 or kv_win.shape[0] != B or kv_win.shape[2] != D or win_end.shape != (Q,):
             raise ValueError("kv_win must be [B, T, D] and win_end [Q]")
         T_raw = kv_win.shape[1]
@@ -569,19 +598,13 @@ def _paged_mqa(name, q, pages, scales, page_table, rows, kv_win, win_end, sink, 
         q_per_seq = Q // B
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", dtype=q.dtype, device=dev)
-    if out.shape != q.shape:
+    o = _check(out, "out", dtype, dev)
+    if out.shape != shape:
         raise ValueError("out must have q's shape")
-    L = _lib.lib()
-    k = () if name != "csa_paged_sparse_mqa" else (rows.shape[1],)
-    with _on(q):
-        nbytes = L.csa_paged_mqa_workspace_bytes(Q, H, D, (k[0] if k else per * page_size) + int(win_len))
-        w = (ws or Workspace(dev)).get(nbytes)
-        rc = getattr(L, name)(
-            _ptr(q), _ptr(pages), _ptr(scales), _ptr(page_table), _ptr(rows), _ptr(kv_win), _ptr(sink), float(scale),
-            _ptr(out), Q, B, H, D, num_pages, page_size, per, *k, int(win_len), _ptr(win_end), T_raw, int(q_per_seq), code,
-            cache, _ptr(w), w.numel(), _stream(dev))
-    _lib.check(name, rc)
+    k = (rows.shape[1],) if sparse else ()
+    nbytes = _lib.lib().csa_paged_mqa_workspace_bytes(Q, H, D, (k[0] if sparse else per * page_size) + win_len)
+    _call(name, dev, q.data_ptr(), p, s, t, r, win, sk, float(scale), o, Q, B, H, D, num_pages, page_size, per, *k, win_len,
+          end, T_raw, int(q_per_seq), code, cache, *_workspace(ws, q.device, dev, nbytes))
     return out
 
 
@@ -590,8 +613,6 @@ def paged_sparse_mqa(q, pages, scales, page_table, idx, kv_win, win_end, sink, s
     """CSA attention over the selected entries of a paged cache + window + sink
     (csa_paged_sparse_mqa). idx int32 [Q, k]; without a window win_len is 0 and
     kv_win, win_end None."""
-    if isinstance(idx, torch.Tensor) and idx.dim() != 2:
-        raise ValueError("idx must be [Q, k]")
     return _paged_mqa("csa_paged_sparse_mqa", q, pages, scales, page_table, idx, kv_win, win_end, sink, scale, win_len,
                       q_per_seq, out, ws)
 
@@ -600,8 +621,6 @@ def paged_hca_mqa(q, pages, scales, page_table, n_cmp, kv_win, win_end, sink, sc
                   q_per_seq=None, out=None, ws: Workspace | None = None):
     """HCA attention over every visible entry of a paged cache + window + sink
     (csa_paged_hca_mqa). n_cmp int32 [Q]."""
-    if isinstance(n_cmp, torch.Tensor) and n_cmp.dim() != 1:
-        raise ValueError("n_cmp must be [Q]")
     return _paged_mqa("csa_paged_hca_mqa", q, pages, scales, page_table, n_cmp, kv_win, win_end, sink, scale, win_len,
                       q_per_seq, out, ws)
 
