@@ -6,7 +6,12 @@
 // of the residual stream that the next layer reads; every sum is fp32.
 //
 // Bytes bound it: x, the residual, h and the output move once each, the row
-// staying in registers between the sum of squares and the output.
+// staying in registers between the sum of squares and the output. With 16 bf16
+// values a thread its instructions come close behind (4,096 rows of 4,096 with
+// 8-bit output: 31 us at one instruction a value and step), so they are packed:
+// x + residual as bf16 pairs (a sum of two bf16 numbers rounds the same from its
+// exact value as from its fp32 one, as what fp32 drops is below 2^-16 of it), the
+// rest as fp32 pairs.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -16,33 +21,57 @@ namespace csa {
 
 namespace {
 
-// 8 consecutive elements as floats.
-__device__ __forceinline__ void load8(const bf16 *p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 8 consecutive elements as they lie in memory, and as pairs of floats.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = u; }
+  __device__ __forceinline__ void add(const Raw8 &o) {
+    auto f = [](uint32_t &a, uint32_t b) { asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b)); };
+    f(u.x, o.u.x), f(u.y, o.u.y), f(u.z, o.u.z), f(u.w, o.u.w);
   }
-}
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(bf16 *p, const float (&v)[8]) {
+  __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = reinterpret_cast<const float4 *>(p)[0];
+    b = reinterpret_cast<const float4 *>(p)[1];
+  }
+  __device__ __forceinline__ void store(float *p) const {
+    reinterpret_cast<float4 *>(p)[0] = a;
+    reinterpret_cast<float4 *>(p)[1] = b;
+  }
+  __device__ __forceinline__ void add(const Raw8 &o) {
+    a = make_float4(a.x + o.a.x, a.y + o.a.y, a.z + o.a.z, a.w + o.a.w);
+    b = make_float4(b.x + o.b.x, b.y + o.b.y, b.z + o.b.z, b.w + o.b.w);
+  }
+  __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const {
+    v[0] = pack2(a.x, a.y), v[1] = pack2(a.z, a.w), v[2] = pack2(b.x, b.y), v[3] = pack2(b.z, b.w);
+  }
+};
+
+__device__ __forceinline__ void store8(bf16 *p, const uint64_t (&v)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    const float2 f = unpack2(v[i]);
+    const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
     w[i] = *reinterpret_cast<const uint32_t *>(&t);
   }
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float *p, const uint64_t (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = unpack2(v[2 * i]), b = unpack2(v[2 * i + 1]);
+    reinterpret_cast<float4 *>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
+  }
 }
 
 // Scale of a group whose largest magnitude is amax.
@@ -53,19 +82,21 @@ __device__ __forceinline__ float group_scale(float amax) {
 
 // The codes of 8 values. v / s as v (1 / s), off by 2^-23 of it at most, next to
 // the 2^-4 of the rounding to E4M3 that follows: the same code but for quotients
-// within 2^-23 of the middle between two. (1 / s overflows for the smallest s: both
-// factors are scaled then.)
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
-  const float up = s < 0x1p-120f ? 0x1p100f : 1.f, inv = 1.f / (s * up);
-  uint32_t w[2];
+// within 2^-23 of the middle between two.
+__device__ __forceinline__ uint2 codes8(const uint64_t (&v)[4], float s) {
+  uint32_t c[4];
+  const float inv = 1.f / s;
+  const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float x[4] = {v[4 * i] * up * inv, v[4 * i + 1] * up * inv, v[4 * i + 2] * up * inv, v[4 * i + 3] * up * inv};
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | hi << 16;
+  for (int i = 0; i < 4; ++i) {
+    float2 x = unpack2(mul2(v[i], inv2));
+    if (s < 0x1p-120f) {  // 1 / s may overflow
+      const float2 y = unpack2(v[i]);
+      x = make_float2(y.x / s, y.y / s);
+    }
+    c[i] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
   }
-  return make_uint2(w[0], w[1]);
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // Reduction over the WPR warps of a row (RPB rows per block), the same in
@@ -86,7 +117,7 @@ __device__ __forceinline__ float row_reduce(float v, float (&red)[RPB][WPR], int
 // WPR warps per row, NV vectors of 8 dims per thread (vector t + 32 WPR i),
 // RPB rows per block.
 template <typename T, int WPR, int NV, int RPB, bool kFp8>
-__global__ void __launch_bounds__(32 * WPR *RPB) add_rmsnorm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(32 * WPR *RPB, 2048 / (32 * WPR * RPB)) add_rmsnorm_kernel(NormArgs a) {
   __shared__ float red[RPB][WPR];
   pdl_wait();
   pdl_release();
@@ -94,44 +125,49 @@ __global__ void __launch_bounds__(32 * WPR *RPB) add_rmsnorm_kernel(NormArgs a) 
   const int t = warp * 32 + lane, nvec = a.D / 8;
   const long long r = (long long)blockIdx.x * RPB + row;
   const bool live = r < a.rows;
-  float v[NV][8], ss = 0.f;
+  uint64_t v[NV][4], ss2 = pack2(0.f, 0.f);
+  Raw8<T> h[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = t + 32 * WPR * i;
     if (live && j < nvec) {
-      load8(static_cast<const T *>(a.x) + r * a.x_stride + 8 * j, v[i]);
+      h[i].load(static_cast<const T *>(a.x) + r * a.x_stride + 8 * j);
       if (a.residual) {
-        float u[8];
-        load8(static_cast<const T *>(a.residual) + r * a.D + 8 * j, u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = to_f(from_f<T>(v[i][e] + u[e]));
+        Raw8<T> u;
+        u.load(static_cast<const T *>(a.residual) + r * a.D + 8 * j);
+        h[i].add(u);
       }
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      h[i] = Raw8<T>{};
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = t + 32 * WPR * i;
-    if (a.residual && live && j < nvec) store8(static_cast<T *>(a.sum_out) + r * a.D + 8 * j, v[i]);
+    if (a.residual && live && j < nvec) h[i].store(static_cast<T *>(a.sum_out) + r * a.D + 8 * j);
+    h[i].pairs(v[i]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+    for (int e = 0; e < 4; ++e) ss2 = fma2(v[i][e], v[i][e], ss2);
   }
+  float ss = unpack2(ss2).x + unpack2(ss2).y;
   ss = row_reduce<WPR, RPB, false>(ss, red, row, warp, lane);
   const float rs = 1.f / sqrtf(ss / (float)a.D + a.eps);
+  const uint64_t rs2 = pack2(rs, rs);
   float amax[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = t + 32 * WPR * i;
     amax[i] = 0.f;
     if (live && j < nvec) {
-      float g[8];
-      load8(a.weight + 8 * j, g);
+      Raw8<float> w;
+      w.load(a.weight + 8 * j);
+      uint64_t g[4];
+      w.pairs(g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[i][e] = v[i][e] * rs * g[e];
-        amax[i] = fmaxf(amax[i], fabsf(v[i][e]));
+      for (int e = 0; e < 4; ++e) {
+        v[i][e] = mul2(mul2(v[i][e], rs2), g[e]);
+        const float2 y = unpack2(v[i][e]);
+        amax[i] = fmaxf(fmaxf(amax[i], fabsf(y.x)), fabsf(y.y));
       }
       if constexpr (!kFp8) store8(static_cast<T *>(a.out) + r * a.D + 8 * j, v[i]);
     }
@@ -145,7 +181,11 @@ __global__ void __launch_bounds__(32 * WPR *RPB) add_rmsnorm_kernel(NormArgs a) 
       for (int i = 0; i < NV; ++i) {
         const int j = t + 32 * WPR * i;
         float m = amax[i];
-        for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float other = __shfl_xor_sync(0xffffffffu, m, o);
+          if (o < lanes) m = fmaxf(m, other);
+        }
         if (live && j < nvec) {
           const float s = group_scale(m);
           *reinterpret_cast<uint2 *>(out + 8 * j) = codes8(v[i], s);
