@@ -215,15 +215,18 @@ __global__ void __launch_bounds__(kThreads) paged_mqa_kernel(PagedMqaArgs a, int
 //   M = max(max_s m_s, sink), L = sum_s l_s 2^(m_s - M) + 2^(sink - M),
 //   out = sum_s O_s 2^(m_s - M) / L.
 // A block takes 512 dims, four a thread, and each thread every split; or (kFew,
-// where that leaves few blocks) 128 dims, and warp w the splits w, w + 4, ... Its
-// bytes are the partials', just written, so L2 serves them; the first of them
-// are on their way while the weights are formed.
+// where that leaves few blocks) 128 dims, and warp w of 8 the splits w, w + 8, ...
+// Its bytes are the partials', just written, so L2 serves them; eight of a thread's
+// are on their way while the first warp forms the weights.
+constexpr int kMergeWarps = 8;
+
 template <typename T, bool kVec, bool kFew>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const float *part_o, const float *part_ml, const float *sink,
-                                                          T *out, int H, int D, int splits) {
-  __shared__ float4 acc_s[kFew ? 4 : 1][32];
+__global__ void __launch_bounds__(kFew ? 32 * kMergeWarps : 128)
+    paged_merge_kernel(const float *part_o, const float *part_ml, const float *sink, T *out, int H, int D, int splits) {
+  __shared__ float4 acc_s[kFew ? kMergeWarps : 1][32];
+  __shared__ float w[kPagedMaxSplits];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kStep = kFew ? 4 : 1;
+  constexpr int kStep = kFew ? kMergeWarps : 1;
   const size_t qh = blockIdx.x;
   const int d0 = (kFew ? 128 : 512) * blockIdx.y, d = d0 + 4 * (kFew ? lane : (int)threadIdx.x);
   const int s0 = kFew ? warp : 0;
@@ -244,24 +247,40 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const float *part_o, c
     }
     return v;
   };
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   float4 v[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) v[i] = load(s0 + kStep * i);
-  const float2 *ml = reinterpret_cast<const float2 *>(part_ml) + qh * splits;
-  const float sk = sink[qh % H] * kLog2e;
-  float M = sk, L = 0.f;
-  for (int s = lane; s < splits; s += 32) M = fmaxf(M, ml[s].x);
-  M = warp_max(M);
-  for (int s = lane; s < splits; s += 32) L = fmaf(ml[s].y, exp2f(ml[s].x - M), L);
-  L = warp_sum(L) + exp2f(sk - M);
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+  if (warp == 0) {
+    constexpr int kPer = kPagedMaxSplits / 32;
+    const float2 *ml = reinterpret_cast<const float2 *>(part_ml) + qh * splits;
+    const float sk = sink[qh % H] * kLog2e;
+    float2 m[kPer];
+    float M = sk, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      m[i] = lane + 32 * i < splits ? ml[lane + 32 * i] : make_float2(-INFINITY, 0.f);
+      M = fmaxf(M, m[i].x);
+    }
+    M = warp_max(M);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      m[i].x = lane + 32 * i < splits ? exp2f(m[i].x - M) : 0.f;
+      L = fmaf(m[i].y, m[i].x, L);
+    }
+    L = warp_sum(L) + exp2f(sk - M);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < splits) w[lane + 32 * i] = m[i].x * inv;
+  }
+  __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = s0; s < splits; s += kStep * kAhead) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (s + kStep * i < splits) {
-        const float c = exp2f(ml[s + kStep * i].x - M);
+        const float c = w[s + kStep * i];
         acc.x = fmaf(c, v[i].x, acc.x);
         acc.y = fmaf(c, v[i].y, acc.y);
         acc.z = fmaf(c, v[i].z, acc.z);
@@ -273,15 +292,18 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const float *part_o, c
   if constexpr (kFew) {
     acc_s[warp][lane] = acc;
     __syncthreads();
-    if (d0 + (int)threadIdx.x < D) {
+    if (threadIdx.x < 128 && d0 + (int)threadIdx.x < D) {
       const float *a = reinterpret_cast<const float *>(acc_s) + threadIdx.x;
-      out[qh * D + d0 + threadIdx.x] = from_f<T>(((a[0] + a[128]) + (a[256] + a[384])) * inv);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMergeWarps; ++i) sum += a[128 * i];
+      out[qh * D + d0 + threadIdx.x] = from_f<T>(sum);
     }
   } else {
     const float o[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (d + e < D) out[qh * D + d + e] = from_f<T>(o[e] * inv);
+      if (d + e < D) out[qh * D + d + e] = from_f<T>(o[e]);
   }
 }
 
@@ -293,8 +315,8 @@ cudaError_t launch_merge(const PagedMqaArgs &a, int splits, cudaStream_t stream)
   const bool few = blocks < 4 * device_sm_count();
   auto kern = D % 4 ? (few ? paged_merge_kernel<T, false, true> : paged_merge_kernel<T, false, false>)
                     : (few ? paged_merge_kernel<T, true, true> : paged_merge_kernel<T, true, false>);
-  const int dims = few ? 128 : 512;
-  return launch_pdl(kern, dim3((unsigned)blocks, (D + dims - 1) / dims), dim3(128), 0, stream, (const float *)a.part_o,
+  const int dims = few ? 128 : 512, threads = few ? 32 * kMergeWarps : 128;
+  return launch_pdl(kern, dim3((unsigned)blocks, (D + dims - 1) / dims), dim3(threads), 0, stream, (const float *)a.part_o,
                     (const float *)a.part_ml, a.sink, static_cast<T *>(a.out), a.H, D, splits);
 }
 

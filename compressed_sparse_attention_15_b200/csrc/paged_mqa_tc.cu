@@ -545,21 +545,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       sm->slot[my_row] = at;
       if (kInt4 && !is_win(li)) {
+        // this lane's row as an address (0: no key); every lane copies pieces of every row
+        const uint64_t code_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.pages) + (uint64_t)at * (kD / 2) : 0;
+        const uint64_t scale_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.scales) + (uint64_t)at * (kD / 16) : 0;
         constexpr int kPer = 2 * NB;  // 16-byte pieces of a row's codes
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int n = 32 * i + lane, rw = n / kPer, c = n - rw * kPer;
-          const long long slot = __shfl_sync(0xffffffffu, at, rw);
-          const uint8_t *src = a.cache.pages + (slot >= 0 ? (size_t)slot * (kD / 2) + 16 * c : 0);
-          cp_async16(codes + (32 * half + rw) * stage_row(NB) + 16 * c, src, slot >= 0);
+          const uint64_t row = __shfl_sync(0xffffffffu, code_row, rw);
+          cp_async16(codes + (32 * half + rw) * stage_row(NB) + 16 * c,
+                     reinterpret_cast<const void *>(row ? row + 16 * c : reinterpret_cast<uint64_t>(a.cache.pages)), row != 0);
         }
         constexpr int kPiece = NB % 4 ? 8 : 16, kPerS = 4 * NB / kPiece;  // pieces of a row's scales
 #pragma unroll
         for (int i = 0; i < kPerS; ++i) {
           const int n = 32 * i + lane, rw = n / kPerS, c = n - rw * kPerS;
-          const long long slot = __shfl_sync(0xffffffffu, at, rw);
-          const uint8_t *src = a.cache.scales + (slot >= 0 ? (size_t)slot * (kD / 16) + kPiece * c : 0);
-          cp_async_piece<kPiece>(scales + (32 * half + rw) * kStageScaleRow + kPiece * c, src, slot >= 0);
+          const uint64_t row = __shfl_sync(0xffffffffu, scale_row, rw);
+          cp_async_piece<kPiece>(scales + (32 * half + rw) * kStageScaleRow + kPiece * c,
+                                 reinterpret_cast<const void *>(row ? row + kPiece * c : reinterpret_cast<uint64_t>(a.cache.scales)),
+                                 row != 0);
         }
       } else if (at >= 0) {  // a bf16 row: into L2, for the copy
         const bf16 *base = is_win(li) ? static_cast<const bf16 *>(a.kv_win) + (size_t)b * a.T_raw * kD
