@@ -28,7 +28,10 @@
 //
 // The kernel is persistent: a block takes items (one split of the row list of 64
 // heads of a query) in turn, and each role runs ahead into the next item, so that
-// its loads, its queries' and its first products overlap the end of the last.
+// its loads, its queries' and its first products overlap the end of the last. Row
+// lists differ in length (a selection ends at its last used slot), so a block
+// claims its next item, by a counter in the workspace, while it works on one: with
+// items dealt out in advance the last block of 148 finished a third after the mean.
 //
 // Roles (640 threads): warps 0-7 widen (or copy bf16 rows), warps 8-15 run the
 // softmax and write the output, warp 16 loads the queries and issues S^T, warp
@@ -70,6 +73,8 @@ struct Small {
   uint64_t q_full, q_empty, o_done, o_free;    // per item: queries loaded / read, O^T made / read
   uint64_t norm_full;                          // per item: norm is there
   uint64_t s_fin, pv_fin;                      // the last products of the block
+  uint64_t item_full[4], item_empty[4];        // ring of the block's items
+  alignas(16) int item[4][8];                  // of struct Item: qv, t0, ntiles, b, nsel, wlo, nwin, w64
   float red[4][kH];
   float mref[kH];
   float alpha[kH];            // what a rescale multiplies by
@@ -98,55 +103,75 @@ static_assert(smem_bytes(8) <= 227 * 1024, "shared memory per block");
 // padded with unused rows to whole tiles: w64), then the compressed rows
 // [w64, w64 + nsel).
 struct Item {
+  int qv;  // query and head group; -1: no more items
   int qq, h0, b;
   int nsel, wlo, nwin, w64;
   int t0, ntiles;
 };
 
-// The device values an item depends on, loaded an item ahead.
-struct Raw {
-  int n, e;
-};
+// The waits of this kernel: one try in line, the rest (with its limit) out of
+// line. Some thirty waits by five roles, each with its own loop, made a kernel of
+// 130 KB, more than the instruction caches hold, and every role slower.
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  return tc::mbar_wait(bar, parity, abort, status, tc::wait_limit_of(status));
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  return tc::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, status);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  return __all_sync(0xffffffffu, wait(bar, parity, abort, status));
+}
 
 // Query qv / 2 and its heads 64 (qv % 2) ... where a query has more than 64 heads, else query qv.
 __device__ __forceinline__ int query_of(const PagedMqaArgs &a, int qv) { return a.H > kH ? qv >> 1 : qv; }
 
-__device__ __forceinline__ Raw load_raw(const PagedMqaArgs &a, int qv, int qvs) {
-  Raw r{a.k, 0};
-  if (qv < qvs) {
-    const int qq = query_of(a, qv);
-    if (!a.idx) r.n = a.n_cmp[qq];
-    if (a.win_len) r.e = a.win_end[qq];
-  }
-  return r;
+// Item number k of the block; false if the wait for it gave up. The whole warp takes part.
+__device__ __forceinline__ bool take_item(const PagedMqaArgs &a, Small *sm, uint32_t k, volatile int *abort, Item &t) {
+  if (!__all_sync(0xffffffffu, wait(&sm->item_full[k & 3], (k >> 2) & 1, abort, a.status))) return false;
+  const int4 u = *reinterpret_cast<const int4 *>(sm->item[k & 3]), v = *reinterpret_cast<const int4 *>(sm->item[k & 3] + 4);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&sm->item_empty[k & 3]);
+  t.qv = u.x;
+  t.t0 = u.y;
+  t.ntiles = u.z;
+  t.b = u.w;
+  t.nsel = v.x;
+  t.wlo = v.y;
+  t.nwin = v.z;
+  t.w64 = v.w;
+  t.qq = query_of(a, t.qv);
+  t.h0 = a.H > kH ? (t.qv & 1) * kH : 0;
+  return true;
 }
 
-__device__ __forceinline__ Item make_item(const PagedMqaArgs &a, int qv, Raw raw, uint32_t *status) {
-  Item t;
-  t.qq = query_of(a, qv);
-  t.h0 = a.H > kH ? (qv & 1) * kH : 0;
-  t.b = t.qq / a.q_per_seq;
-  t.nsel = a.idx ? a.k : clamp_count(raw.n, (int)a.cache.capacity(), status);
-  t.wlo = t.nwin = 0;
+// (nsel, wlo, nwin) of an item: the count clamped, a selection up to its last used slot.
+__device__ __forceinline__ int3 item_rows(const PagedMqaArgs &a, int qv, int lane, uint32_t *status) {
+  const int qq = query_of(a, qv);
+  int3 v = make_int3(0, 0, 0);
+  int e = a.win_len ? a.win_end[qq] : 0;
+  if (a.idx) {
+#pragma unroll 1
+    for (int i0 = a.k - 128; v.x == 0 && i0 > -128; i0 -= 128) {
+      int last = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + lane + 32 * u;
+        if (i >= 0 && a.idx[(size_t)qq * a.k + i] != -1) last = i + 1;
+      }
+      v.x = __reduce_max_sync(0xffffffffu, last);
+    }
+  } else {
+    v.x = clamp_count(a.n_cmp[qq], (int)a.cache.capacity(), status);
+  }
   if (a.win_len) {
-    int e = raw.e;
     if (e < 0 || e >= a.T_raw) {
       raise_status(status, CSA_STATUS_BAD_WINDOW);
       e = e < 0 ? 0 : a.T_raw - 1;
     }
-    t.wlo = max(0, e - a.win_len + 1);
-    t.nwin = e - t.wlo + 1;
+    v.y = max(0, e - a.win_len + 1);
+    v.z = e - v.y + 1;
   }
-  t.w64 = (t.nwin + kRows - 1) / kRows * kRows;
-  const int tiles = (t.w64 + t.nsel + kRows - 1) / kRows;
-  t.t0 = 0;
-  t.ntiles = tiles;
-  if (gridDim.y > 1) {
-    const int splits = gridDim.y, split = blockIdx.y, base = tiles / splits, rest = tiles - base * splits;
-    t.t0 = split * base + min(split, rest);
-    t.ntiles = base + (split < rest ? 1 : 0);
-  }
-  return t;
+  return v;
 }
 
 // 32 bytes of codes and 4 of scales: 64 dims of one row.
@@ -164,11 +189,22 @@ __device__ __forceinline__ void load_packed(Packed &u, uint32_t codes, uint32_t 
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u.s) : "r"(scales));
 }
 
-// n bytes (8 or 16), or zeros.
+// 8 or 16 bytes from global memory, or zeros where there is no source. (Zeros are
+// stored: a copy of no bytes still asks for its address, the same one everywhere.
+// Predicated, as a branch a piece cost 7 % of a prefill chunk.)
 template <int kBytes>
-__device__ __forceinline__ void cp_async_piece(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(valid ? kBytes : 0)
-               : "memory");
+__device__ __forceinline__ void copy_piece(uint32_t dst, uint64_t src) {
+  if constexpr (kBytes == 16)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u64 p, %1, 0;\n\t"
+        "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t@!p st.shared.v4.b32 [%0], {%2, %2, %2, %2};\n\t}" ::"r"(dst),
+        "l"(src), "r"(0)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u64 p, %1, 0;\n\t"
+        "@p cp.async.ca.shared.global [%0], [%1], 8;\n\t@!p st.shared.v2.b32 [%0], {%2, %2};\n\t}" ::"r"(dst), "l"(src), "r"(0)
+        : "memory");
 }
 
 // An arrival on `bar` once this thread's copies so far have landed.
@@ -228,31 +264,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // The 64 dims of `u` into the 128-byte line whose chunk 0 is at `chunk0` (16-byte chunks, swizzled).
 __device__ __forceinline__ void store_widened(const Packed &u, uint32_t chunk0) {
   // per 16 dims: s and -136 s, in both halves of a register
   uint32_t sc[4], off[4];
-  if (((u.s | (u.s + 0x01010101u)) & 0x80808080u) == 0) {
-    // E4M3's exponent and mantissa, moved to where bf16 has them, are s 2^-120 (subnormals too)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint32_t t = __byte_perm(u.s, 0, 0x4040u | (0x0101u * g)) << 4;
-      sc[g] = mul_bf16x2(t, 0x7b807b80u);   // 2^120
-      off[g] = mul_bf16x2(t, 0xff08ff08u);  // -136 2^120
-    }
-  } else {  // a NaN or a sign among the scales
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float s = e4m3_value((uint8_t)(u.s >> (8 * g)));
-      sc[g] = bf16x2_dup(s);
-      off[g] = bf16x2_dup(-136.f * s);
-    }
+  for (int p = 0; p < 2; ++p) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u.s >> (16 * p)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    sc[2 * p] = bf16x2_dup(f.x);
+    sc[2 * p + 1] = bf16x2_dup(f.y);
+    off[2 * p] = bf16x2_dup(-136.f * f.x);
+    off[2 * p + 1] = bf16x2_dup(-136.f * f.y);
   }
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
@@ -267,27 +290,25 @@ __device__ __forceinline__ void store_widened(const Packed &u, uint32_t chunk0) 
 template <int NB>
 __device__ __forceinline__ void issue_s(uint32_t tmem_s, uint64_t kv, uint64_t q, int part) {
   constexpr uint32_t idesc = tc::idesc_bf16(64, 64, 0, 0);
-  kv += (uint64_t)((part * 4 * kBoxBytes) >> 4);
-  q += (uint64_t)((part * 4 * kQBoxBytes) >> 4);
+  const int b0 = 4 * part, b1 = min(NB, b0 + 4);
+  kv += (uint64_t)(b0 * (kBoxBytes >> 4));
+  q += (uint64_t)(b0 * (kQBoxBytes >> 4));
+#pragma unroll 1
+  for (int bx = b0; bx < b1; ++bx, kv += kBoxBytes >> 4, q += kQBoxBytes >> 4) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j < 4 * NB - 16 * part)
-      tc::mma_bf16(tmem_s, kv + (uint64_t)(((j >> 2) * kBoxBytes + (j & 3) * 32) >> 4),
-                   q + (uint64_t)(((j >> 2) * kQBoxBytes + (j & 3) * 32) >> 4), idesc, part > 0 || j > 0);
+    for (int j = 0; j < 4; ++j) tc::mma_bf16(tmem_s, kv + 2 * j, q + 2 * j, idesc, bx > 0 || j > 0);
+  }
 }
 template <int NB>
 __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint64_t v, uint64_t p, bool first, int part) {
   constexpr uint32_t idesc = tc::idesc_bf16(128, 64, 1, 1);
-  tmem_o += 128 * part;
-  v += (uint64_t)((part * 4 * kBoxBytes) >> 4);
+  const int m0 = 2 * part, m1 = min(NB / 2, m0 + 2);
+  v += (uint64_t)(m0 * (2 * kBoxBytes >> 4));
+  tmem_o += 64 * m0;
+#pragma unroll 1
+  for (int m = m0; m < m1; ++m, tmem_o += 64, v += 2 * kBoxBytes >> 4) {
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    if (m < NB / 2 - 2 * part) {
-#pragma unroll
-      for (int j = 0; j < kRows / 16; ++j)
-        tc::mma_bf16(tmem_o + 64 * m, v + (uint64_t)((2 * m * kBoxBytes + j * 2048) >> 4), p + (uint64_t)((j * 2048) >> 4),
-                     idesc, j > 0 || !first);
-    }
+    for (int j = 0; j < kRows / 16; ++j) tc::mma_bf16(tmem_o, v + 128 * j, p + 128 * j, idesc, j > 0 || !first);
   }
 }
 
@@ -297,7 +318,7 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint64_t v, uint64_t p
 // 128-dim chunk, m % 2: half of the warp's TMEM quarter), each turned in registers
 // so that 4 lanes write a 32-byte sector of a head's row.
 template <int NB>
-__device__ __forceinline__ void write_out(const PagedMqaArgs &a, uint32_t tmem, const float *norm, size_t qh, int heads,
+__device__ __noinline__ void write_out(const PagedMqaArgs &a, uint32_t tmem, const float *norm, size_t qh, int heads,
                                           int quarter, int m0, int m1, bool some, uint64_t *o_free) {
   constexpr int kD = 64 * NB;
   const int lane = threadIdx.x & 31, rq = lane >> 2, cq = lane & 3;
@@ -354,7 +375,8 @@ __device__ __forceinline__ void write_out(const PagedMqaArgs &a, uint32_t tmem, 
 // NB: head_dim / 64. kInt4: the cache is in 4 bits.
 template <int NB, bool kInt4>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_mqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, PagedMqaArgs a, int qvs, float scale_log2) {
+    paged_mqa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_win, PagedMqaArgs a,
+                        int qvs, float scale_log2) {
   constexpr int kD = 64 * NB;
   constexpr uint32_t kTileBytes = NB * kBoxBytes, kQBytes = NB * kQBoxBytes;
   constexpr uint32_t kColS = 64 * (NB / 2);  // O^T chunk m at columns 64 m, S^T buffer j at kColS + 64 j
@@ -386,6 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&sm->o_done, 1);
     tc::mbar_init(&sm->o_free, 32 * (kLoadWarps + kSoftWarps));
     tc::mbar_init(&sm->norm_full, kH);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sm->item_full[i], 1);
+      tc::mbar_init(&sm->item_empty[i], kThreads / 32);
+    }
     tc::mbar_init(&sm->s_fin, 1);
     tc::mbar_init(&sm->pv_fin, 1);
     sm->abort = 0;
@@ -399,9 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   volatile int *abort = &sm->abort;
   pdl_wait();
-  const uint64_t lim = tc::wait_limit_of(a.status);
   pdl_release();
-  Raw raw = load_raw(a, blockIdx.x, qvs);
 
   if (warp < kLoadWarps) {
     // ------------------------------------------------------------ widening
@@ -413,11 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // Half of an item's output is these warps' to write. They do so when both
     // tile buffers hold tiles of the items after it, and have nothing else to do.
+    int tma_last = -1;  // the last tile that this thread had copied in bulk
     int out_qv = -1;
     uint32_t out_at = 0, done = 0;  // the tile before which it is written; items written
     auto output = [&] {
-      ok = ok && tc::mbar_wait(&sm->norm_full, done & 1, abort, a.status, lim);
-      ok = ok && tc::mbar_wait(&sm->o_done, done & 1, abort, a.status, lim);
+      ok = ok && wait(&sm->norm_full, done & 1, abort, a.status);
+      ok = ok && wait(&sm->o_done, done & 1, abort, a.status);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
       const int half = warp >> 2, h0 = (a.H > kH ? (out_qv & 1) * kH : 0) + 32 * half;
@@ -427,16 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++done;
       out_qv = -1;
     };
-    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
-      const Item L = make_item(a, qv, raw, nullptr);
-      raw = load_raw(a, qv + gridDim.x, qvs);
+    for (uint32_t k = 0; ok; ++k) {
+      Item L;
+      ok = take_item(a, sm, k, abort, L);
+      if (!ok || L.qv < 0) break;
       for (int li = 0; li < L.ntiles; ++li, ++T) {
         const int g = T & 1;
         if (out_qv >= 0 && T == out_at) output();
         if (!ok) break;
         const uint32_t free_phase = ((T >> 1) & 1) ^ 1, line = kv_base + g * kTileBytes + my_row * 128 + ((lane & 7) << 4);
         const bool in_win = (L.t0 + li) * kRows < L.w64;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->stage_full, T & 1, abort, a.status, lim));
+        ok = warp_wait(&sm->stage_full, T & 1, abort, a.status);
         if (!ok) break;
         const long long slot = sm->slot[my_row];
         if (kInt4 && !in_win) {
@@ -450,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tc::mbar_arrive(&sm->stage_empty);
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->kv_empty[g][i], free_phase, abort, a.status, lim));
+            ok = warp_wait(&sm->kv_empty[g][i], free_phase, abort, a.status);
             if (!ok) break;
             if (i == 0 && lane < kRowsPerWarp) sm->valid[g][my_row] = slot >= 0;
             const int s = (lane >> 3) + 4 * i;
@@ -463,9 +489,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tc::mbar_arrive(&sm->stage_empty);
 #pragma unroll
           for (int i = 0; i < kParts; ++i)
-            ok = ok && tc::mbar_wait(&sm->kv_empty[g][i], free_phase, abort, a.status, lim);
+            ok = ok && wait(&sm->kv_empty[g][i], free_phase, abort, a.status);
           ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
+          const int r0 = (L.t0 + li) * kRows;
+          if (ok && in_win && r0 + kRows <= L.nwin) {
+            // 64 rows of the window on end: bulk copies, which land while the next tile is widened. (Not so where
+            // rows of the tile lie outside the window: those must not be read.)
+            if (lane < kRowsPerWarp) sm->valid[g][my_row] = 1;
+            if (warp == 0 && lane == 0) {
+#pragma unroll
+              for (int i = 0; i < kParts; ++i) {
+                const int b0 = 4 * i, b1 = min(NB, b0 + 4);
+                tc::mbar_arrive_expect_tx(&sm->kv_full[g][i], (b1 - b0) * kBoxBytes);
+                for (int bx = b0; bx < b1; ++bx)
+                  tc::tma_load_2d(kv + g * kTileBytes + bx * kBoxBytes, &tm_win, 64 * bx, L.b * a.T_raw + L.wlo + r0,
+                                  &sm->kv_full[g][i]);
+              }
+              tma_last = T;
+            } else {
+#pragma unroll
+              for (int i = 0; i < kParts; ++i) tc::mbar_arrive(&sm->kv_full[g][i]);
+            }
+          } else if (ok) {
             if (lane < kRowsPerWarp) sm->valid[g][my_row] = slot >= 0;
             const bf16 *base = in_win ? static_cast<const bf16 *>(a.kv_win) + (size_t)L.b * a.T_raw * kD
                                       : reinterpret_cast<const bf16 *>(a.cache.pages);
@@ -473,9 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int rw = 0; rw < kRowsPerWarp; ++rw) {
               const long long at = __shfl_sync(0xffffffffu, slot, rw);
               const uint32_t dst = kv_base + g * kTileBytes + (kRowsPerWarp * warp + rw) * 128;
-              const bf16 *src = at >= 0 ? base + (size_t)at * kD : static_cast<const bf16 *>(a.q);
+              const uint64_t src = at >= 0 ? reinterpret_cast<uint64_t>(base + (size_t)at * kD) : 0;
               for (int c16 = lane; c16 < 8 * NB; c16 += 32)  // 16-byte piece c16 of the row
-                cp_async16(dst + (c16 >> 3) * kBoxBytes + (((c16 & 7) ^ rw) << 4), at >= 0 ? src + c16 * 8 : src, at >= 0);
+                copy_piece<16>(dst + (c16 >> 3) * kBoxBytes + (((c16 & 7) ^ rw) << 4), src ? src + 16 * c16 : 0);
             }
             cp_async_wait_all();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -488,11 +533,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && L.ntiles > 0) {
         // (an item of one tile may end before the output of the one before it is due)
         if (out_qv >= 0) output();
-        out_qv = qv;
+        out_qv = L.qv;
         out_at = T + 2;
       }
     }
     if (out_qv >= 0) output();
+    if (!ok && tma_last >= 0)  // (nothing is in flight when the block ends; without a fault every tile was used)
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) tc::mbar_drain(&sm->kv_full[tma_last & 1][i], (tma_last >> 1) & 1);
   } else if (warp >= kFetchWarp0) {
     // ------------------------------------------------------------ lookups and fetches
     // A lane looks one row up; a warp copies its 32 rows.
@@ -500,9 +548,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t codes = tc::smem_u32(stage), scales = codes + kRows * stage_row(NB);
     uint32_t T = 0;
     bool ok = true;
-    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
-    const Item L = make_item(a, qv, raw, nullptr);
-    raw = load_raw(a, qv + gridDim.x, qvs);
+    // The first of these warps also makes the block's items, the next when it has
+    // fetched the last tile of one: the tiles in flight then last longer than the
+    // claim and the loads take, and the blocks end as evenly as may be.
+    const bool maker = warp == kFetchWarp0;
+    for (uint32_t k = 0; ok; ++k) {
+    if (maker) {
+      int next = blockIdx.x;  // (the first item is the block's own)
+      if (k > 0) {
+        next = qvs;
+        if (qvs > (int)gridDim.x) next = __shfl_sync(0xffffffffu, lane == 0 ? (int)(gridDim.x + atomicAdd(a.status + 4, 1u)) : 0, 0);
+      }
+      const int3 v = next < qvs ? item_rows(a, next, lane, blockIdx.y == 0 && lane == 0 ? a.status : nullptr) : make_int3(0, 0, 0);
+      ok = warp_wait(&sm->item_empty[k & 3], ((k >> 2) & 1) ^ 1, abort, a.status);
+      if (lane == 0) {
+        const int w64 = (v.z + kRows - 1) / kRows * kRows, tiles = (w64 + v.x + kRows - 1) / kRows;
+        const int splits = gridDim.y, split = blockIdx.y, base = tiles / splits, rest = tiles - base * splits;
+        *reinterpret_cast<int4 *>(sm->item[k & 3]) = make_int4(next < qvs ? next : -1, split * base + min(split, rest),
+                                                               base + (split < rest ? 1 : 0), query_of(a, next) / a.q_per_seq);
+        *reinterpret_cast<int4 *>(sm->item[k & 3] + 4) = make_int4(v.x, v.y, v.z, w64);
+        tc::mbar_arrive(&sm->item_full[k & 3]);
+      }
+    }
+    Item L;
+    ok = take_item(a, sm, k, abort, L);
+    if (!ok || L.qv < 0) break;
     const int t0 = L.t0, ntiles = L.ntiles, b = L.b, qq = L.qq;
     auto is_win = [&](int li) { return (t0 + li) * kRows < L.w64; };
     // The lookup of this lane's row of tile li in three steps, each one load: the
@@ -541,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int2 p1 = page_of(1, e1);
     long long at = row_of(0, p0);
     for (int li = 0; li < ntiles; ++li, ++T) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->stage_empty, (T & 1) ^ 1, abort, a.status, lim));
+      ok = warp_wait(&sm->stage_empty, (T & 1) ^ 1, abort, a.status);
       if (!ok) break;
       sm->slot[my_row] = at;
       if (kInt4 && !is_win(li)) {
@@ -549,21 +619,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t code_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.pages) + (uint64_t)at * (kD / 2) : 0;
         const uint64_t scale_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.scales) + (uint64_t)at * (kD / 16) : 0;
         constexpr int kPer = 2 * NB;  // 16-byte pieces of a row's codes
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < kPer; ++i) {
           const int n = 32 * i + lane, rw = n / kPer, c = n - rw * kPer;
           const uint64_t row = __shfl_sync(0xffffffffu, code_row, rw);
-          cp_async16(codes + (32 * half + rw) * stage_row(NB) + 16 * c,
-                     reinterpret_cast<const void *>(row ? row + 16 * c : reinterpret_cast<uint64_t>(a.cache.pages)), row != 0);
+          copy_piece<16>(codes + (32 * half + rw) * stage_row(NB) + 16 * c, row ? row + 16 * c : 0);
         }
         constexpr int kPiece = NB % 4 ? 8 : 16, kPerS = 4 * NB / kPiece;  // pieces of a row's scales
 #pragma unroll
         for (int i = 0; i < kPerS; ++i) {
           const int n = 32 * i + lane, rw = n / kPerS, c = n - rw * kPerS;
           const uint64_t row = __shfl_sync(0xffffffffu, scale_row, rw);
-          cp_async_piece<kPiece>(scales + (32 * half + rw) * kStageScaleRow + kPiece * c,
-                                 reinterpret_cast<const void *>(row ? row + kPiece * c : reinterpret_cast<uint64_t>(a.cache.scales)),
-                                 row != 0);
+          copy_piece<kPiece>(scales + (32 * half + rw) * kStageScaleRow + kPiece * c, row ? row + kPiece * c : 0);
         }
       } else if (at >= 0) {  // a bf16 row: into L2, for the copy
         const bf16 *base = is_win(li) ? static_cast<const bf16 *>(a.kv_win) + (size_t)b * a.T_raw * kD
@@ -582,22 +649,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ queries, S^T
     // (the whole warp runs the loops of the two issuers; one lane issues)
     const uint64_t ad_kv = tc::sw128_desc(tc::smem_u32(kv), 16, 1024), bd_q = tc::sw128_desc(tc::smem_u32(qs), 16, 1024);
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, a.status, lim));
-    };
+    auto ready = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
     uint32_t T = 0, done = 0;  // tiles and items (with tiles) so far
     bool ok = true;
-    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
-      const Item it = make_item(a, qv, raw, nullptr);
-      raw = load_raw(a, qv + gridDim.x, qvs);
+    for (uint32_t k = 0; ok; ++k) {
+      Item it;
+      ok = take_item(a, sm, k, abort, it);
+      if (!ok || it.qv < 0) break;
       if (it.ntiles == 0) continue;
-      if (done > 0 && !(ok = wait(&sm->q_empty, (done - 1) & 1))) break;
+      if (done > 0 && !(ok = ready(&sm->q_empty, (done - 1) & 1))) break;
       if (tc::elect_one()) {
         tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
         for (int bx = 0; bx < NB; ++bx) tc::tma_load_3d(qs + bx * kQBoxBytes, &tm_q, bx * 64, it.h0, it.qq, &sm->q_full);
       }
       __syncwarp();
-      if (!(ok = wait(&sm->q_full, done & 1))) {
+      if (!(ok = ready(&sm->q_full, done & 1))) {
         if (tc::elect_one()) tc::mbar_drain(&sm->q_full, done & 1);  // (nothing is in flight when the block ends)
         break;
       }
@@ -607,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // after P.V(T - 2))
 #pragma unroll 1
         for (int i = 0; i < kParts; ++i) {
-          if (!(ok = wait(&sm->kv_full[buf][i], (T >> 1) & 1))) break;
+          if (!(ok = ready(&sm->kv_full[buf][i], (T >> 1) & 1))) break;
           tc::fence_after_sync();
           if (tc::elect_one())
             issue_s<NB>(tmem + kColS + 64 * buf, ad_kv + (uint64_t)((buf * kTileBytes) >> 4), bd_q, i);
@@ -631,23 +697,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ P.V
     const uint64_t ad_v = tc::sw128_desc(tc::smem_u32(kv), kBoxBytes, 1024);
     const uint64_t bd_p = tc::sw128_desc(tc::smem_u32(ps), kPBytes, 1024);
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, a.status, lim));
-    };
+    auto ready = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
     uint32_t T = 0, done = 0;
     bool ok = true;
-    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
-      const int ntiles = make_item(a, qv, raw, nullptr).ntiles;
-      raw = load_raw(a, qv + gridDim.x, qvs);
+    for (uint32_t k = 0; ok; ++k) {
+      Item it;
+      ok = take_item(a, sm, k, abort, it);
+      if (!ok || it.qv < 0) break;
+      const int ntiles = it.ntiles;
       if (ntiles == 0) continue;
-      if (done > 0 && !(ok = wait(&sm->o_free, (done - 1) & 1))) break;
+      if (done > 0 && !(ok = ready(&sm->o_free, (done - 1) & 1))) break;
       for (int li = 0; li < ntiles; ++li, ++T) {
         const int buf = T & 1;
-        for (int i = 0; i < kParts; ++i) ok = ok && wait(&sm->kv_full[buf][i], (T >> 1) & 1);  // (the tile's writes)
-        if (!ok || !(ok = wait(&sm->p_full, T & 1))) break;
+        for (int i = 0; i < kParts; ++i) ok = ok && ready(&sm->kv_full[buf][i], (T >> 1) & 1);  // (the tile's writes)
+        if (!ok || !(ok = ready(&sm->p_full, T & 1))) break;
         tc::fence_after_sync();
         if (tc::elect_one()) {
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < kParts; ++i) {
             issue_pv<NB>(tmem, ad_v + (uint64_t)((buf * kTileBytes) >> 4), bd_p, li == 0, i);
             tc::commit(&sm->kv_empty[buf][i]);
@@ -682,18 +748,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t T = 0, done = 0;  // tiles so far, items with tiles so far
     const int splits = gridDim.y, split = blockIdx.y;
-    for (int qv = blockIdx.x; ok && qv < qvs; qv += gridDim.x) {
-    const Item it = make_item(a, qv, raw, threadIdx.x == 32 * kSoftWarp0 && split == 0 ? a.status : nullptr);
-    raw = load_raw(a, qv + gridDim.x, qvs);
+    for (uint32_t k = 0; ok; ++k) {
+    Item it;
+    ok = take_item(a, sm, k, abort, it);
+    if (!ok || it.qv < 0) break;
     const int nh = min(kH, a.H - it.h0);
-    uint64_t nm[4], l[4];  // per pair of heads: minus the running maximum (of log2 logits), the running sum
+    uint64_t nm[4], l[4];  // per pair of heads: minus the reference (of log2 logits), the running sum
+    bool fresh = true;     // some of this thread's heads have had no row
 #pragma unroll
-    for (int c = 0; c < 4; ++c) nm[c] = pack2(-kFloor, -kFloor), l[c] = pack2(0.f, 0.f);
+    for (int c = 0; c < 4; ++c) nm[c] = l[c] = pack2(0.f, 0.f);
     for (int li = 0; li < it.ntiles; ++li, ++T) {
       const int buf = T & 1;
       // (kv_full too: the row flags are the loaders' own writes)
-      bool got = tc::mbar_wait(&sm->kv_full[buf][0], (T >> 1) & 1, abort, a.status, lim);
-      got = got && tc::mbar_wait(&sm->s_full[buf], (T >> 1) & 1, abort, a.status, lim);
+      bool got = wait(&sm->kv_full[buf][0], (T >> 1) & 1, abort, a.status);
+      got = got && wait(&sm->s_full[buf], (T >> 1) & 1, abort, a.status);
       got = __all_sync(0xffffffffu, got);
       tc::fence_after_sync();
       const bool validA = sm->valid[buf][rowA], validB = sm->valid[buf][rowB];
@@ -701,13 +769,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t v[16];
       tmem_ld_16x256b_x4(tmem + lane_off + kColS + 64 * buf + 32 * half, v);
       tc::tmem_ld_wait();
-      // y = logit - running maximum, in log2 units; rows without a key are -inf
+      // y = logit - reference, in log2 units; rows without a key are -inf. A
+      // head's reference moves only when some logit of a tile exceeds it by more
+      // than 2^8, and on its first row (it is 0 until then, and not final).
       float2 yA[4], yB[4];
-      auto logits = [&](const uint64_t (&minus)[4]) {
+      bool rescale = false;
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          yA[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), scale2, minus[c]));
-          yB[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), scale2, minus[c]));
+          yA[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), scale2, nm[c]));
+          yB[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), scale2, nm[c]));
         }
         if (!full) {
 #pragma unroll
@@ -716,23 +789,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!validB) yB[c] = make_float2(-INFINITY, -INFINITY);
           }
         }
-      };
-      logits(nm);
-      // The running maximum moves only when some logit of the tile exceeds it
-      // by more than 2^8 (always on the first row).
-      float top = -INFINITY;
+        if (pass) break;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) top = fmaxf(fmaxf(top, fmaxf(yA[c].x, yA[c].y)), fmaxf(yB[c].x, yB[c].y));
-      bool rescale = false;
-      if (bar_any(1 + half, 128, top > kRescaleLog2 || !(got && ok))) {
+        for (int c = 0; c < 4; ++c) top = fmaxf(fmaxf(top, fmaxf(yA[c].x, yA[c].y)), fmaxf(yB[c].x, yB[c].y));
+        if (!bar_any(1 + half, 128, top > kRescaleLog2 || fresh || !(got && ok))) break;
         if (bar_any(1 + half, 128, !(got && ok))) {  // S^T(li) missing, or the previous P.V never completed
           ok = false;
           break;
         }
         // per-head tile maximum: over the thread's two rows, then over the 8
         // lanes of the same cq, then over the 4 warps
-        const uint64_t zero[4] = {0, 0, 0, 0};
-        logits(zero);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float2 mx = make_float2(fmaxf(yA[c].x, yB[c].x), fmaxf(yA[c].y, yB[c].y));
@@ -748,25 +814,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int h = 32 * half + lane;
           const float tm = fmaxf(fmaxf(sm->red[0][h], sm->red[1][h]), fmaxf(sm->red[2][h], sm->red[3][h]));
           const float mo = sm->mref[h];
-          const bool up = tm > mo + kRescaleLog2;
-          if (up) sm->mref[h] = tm;
-          sm->alpha[h] = up ? exp2f(mo - tm) : 1.f;
-          const bool any = __any_sync(0xffffffffu, up && mo != kFloor);
+          const bool first = mo == kFloor, up = first ? tm != -INFINITY : tm > kRescaleLog2;
+          if (up) sm->mref[h] = first ? tm : mo + tm;
+          sm->alpha[h] = up && !first ? exp2f(-tm) : 1.f;
+          const bool any = __any_sync(0xffffffffu, up && !first);
           if (lane == 0) sm->rescale[half] = any ? 1 : 0;
         }
         named_sync(1 + half, 128);
         rescale = sm->rescale[half] != 0;
+        fresh = false;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2 m = *reinterpret_cast<const float2 *>(&sm->mref[32 * half + 8 * c + 2 * cq]);
-          nm[c] = pack2(-m.x, -m.y);
+          fresh |= m.x == kFloor || m.y == kFloor;
+          nm[c] = pack2(m.x == kFloor ? 0.f : -m.x, m.y == kFloor ? 0.f : -m.y);
           if (rescale) {
             const float2 al = *reinterpret_cast<const float2 *>(&sm->alpha[32 * half + 8 * c + 2 * cq]);
-            l[c] = fma2(l[c], pack2(al.x, al.y), 0);
+            l[c] = mul2(l[c], pack2(al.x, al.y));
           }
         }
-        logits(nm);
       }
+      if (!ok) break;
       // P = 2^y, rounded to bf16 and summed per head. The sums take the same
       // bf16 weights as P.V, so that a dominant row's weight (up to 2^8 between
       // rescales) cancels exactly.
@@ -783,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P.V of the tile before has to be complete before P^T, and where the
       // maximum moved O^T too, are written again.
       if (T > 0) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm->pv_done[(T - 1) & 3], ((T - 1) >> 2) & 1, abort, a.status, lim));
+        ok = warp_wait(&sm->pv_done[(T - 1) & 3], ((T - 1) >> 2) & 1, abort, a.status);
         tc::fence_after_sync();
       }
       stmatrix_x4(pdst, pA[0], pB[0], pA[1], pB[1]);
@@ -840,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // These warps' half of the output (all of it where the item has no tiles).
     const bool some = it.ntiles > 0;
     if (some) {
-      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm->o_done, done & 1, abort, a.status, lim));
+      ok = __all_sync(0xffffffffu, ok && wait(&sm->o_done, done & 1, abort, a.status));
       tc::fence_after_sync();
       ++done;
     }
@@ -855,12 +923,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
+  // the last block returns the counters to zero for the next launch
+  if (threadIdx.x == 0 && qvs > (int)gridDim.x && atomicAdd(a.status + 5, 1u) == gridDim.x * gridDim.y - 1) {
+    a.status[4] = 0;
+    a.status[5] = 0;
+  }
 }
 
 bool aligned(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 template <int NB, bool kInt4>
-cudaError_t launch_nb(const PagedMqaArgs &a, const CUtensorMap &tm_q, int splits, cudaStream_t stream) {
+cudaError_t launch_nb(const PagedMqaArgs &a, const CUtensorMap &tm_q, const CUtensorMap &tm_win, int splits, cudaStream_t stream) {
   static DeviceOnce attr;
   once_per_device(attr, [] {
     cudaFuncSetAttribute(paged_mqa_tc_kernel<NB, kInt4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(NB));
@@ -871,7 +944,7 @@ cudaError_t launch_nb(const PagedMqaArgs &a, const CUtensorMap &tm_q, int splits
   if (qvs > 0x7fffffffLL - sms) return cudaErrorInvalidValue;  // (item numbers pass the last by a grid)
   const long long most = sms / splits > 0 ? sms / splits : 1;
   return launch_pdl(paged_mqa_tc_kernel<NB, kInt4>, dim3((unsigned)(qvs < most ? qvs : most), splits), dim3(kThreads),
-                    smem_bytes(NB), stream, tm_q, a, (int)qvs, a.scale * kLog2e);
+                    smem_bytes(NB), stream, tm_q, tm_win, a, (int)qvs, a.scale * kLog2e);
 }
 
 }  // namespace
@@ -898,19 +971,21 @@ cudaError_t launch_paged_mqa_tc(const PagedMqaArgs &args, void *partials, cudaSt
   if (!aligned(a.cache.pages, 16) || !aligned(a.cache.scales, 16)) return cudaSuccess;
   CUtensorMap tm_q;
   if (!make_tmap_bf16_3d(&tm_q, a.q, D, a.H, a.Q, 64, kH)) return cudaSuccess;
+  CUtensorMap tm_win = tm_q;
+  if (a.win_len && !make_tmap_bf16_2d(&tm_win, a.kv_win, D, (uint64_t)a.B * a.T_raw, D * 2, 64, kRows)) return cudaSuccess;
   const int splits = paged_mqa_tc_splits(a.Q, a.H, D, a.rows_max);
   paged_mqa_carve(a, partials, splits);
   *taken = true;
   cudaError_t e = cudaErrorInvalidValue;
   switch (2 * (D / 128) + int4) {
-    case 2: e = launch_nb<2, false>(a, tm_q, splits, stream); break;
-    case 3: e = launch_nb<2, true>(a, tm_q, splits, stream); break;
-    case 4: e = launch_nb<4, false>(a, tm_q, splits, stream); break;
-    case 5: e = launch_nb<4, true>(a, tm_q, splits, stream); break;
-    case 6: e = launch_nb<6, false>(a, tm_q, splits, stream); break;
-    case 7: e = launch_nb<6, true>(a, tm_q, splits, stream); break;
-    case 8: e = launch_nb<8, false>(a, tm_q, splits, stream); break;
-    case 9: e = launch_nb<8, true>(a, tm_q, splits, stream); break;
+    case 2: e = launch_nb<2, false>(a, tm_q, tm_win, splits, stream); break;
+    case 3: e = launch_nb<2, true>(a, tm_q, tm_win, splits, stream); break;
+    case 4: e = launch_nb<4, false>(a, tm_q, tm_win, splits, stream); break;
+    case 5: e = launch_nb<4, true>(a, tm_q, tm_win, splits, stream); break;
+    case 6: e = launch_nb<6, false>(a, tm_q, tm_win, splits, stream); break;
+    case 7: e = launch_nb<6, true>(a, tm_q, tm_win, splits, stream); break;
+    case 8: e = launch_nb<8, false>(a, tm_q, tm_win, splits, stream); break;
+    case 9: e = launch_nb<8, true>(a, tm_q, tm_win, splits, stream); break;
   }
   return e == cudaSuccess && splits > 1 ? launch_paged_merge(a, splits, stream) : e;
 }

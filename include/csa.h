@@ -555,8 +555,9 @@ int csa_paged_read(const void *pages, const uint8_t *scales, const int32_t *page
  * Entries past n_cmp, unlisted entries and rows outside the window are never
  * read: what lies there (a NaN, say) has no effect.
  * Workspace: csa_paged_mqa_workspace_bytes(Q, H, D, rows), rows = k + win_len
- * or pages_per_seq * page_size + win_len. Calls that share one must not
- * overlap on the GPU.
+ * or pages_per_seq * page_size + win_len. Its bytes 16..23 hold counters: zero
+ * before the first call, like the status word, and left at zero by every call.
+ * Calls that share a workspace must not overlap on the GPU.
  * ---------------------------------------------------------------------- */
 size_t csa_paged_mqa_workspace_bytes(int Q, int H, int D, int rows_max);
 int csa_paged_sparse_mqa(const void *q, const void *pages, const uint8_t *scales, const int32_t *page_table,
