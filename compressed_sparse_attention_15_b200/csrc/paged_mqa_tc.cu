@@ -497,10 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // rows of the tile lie outside the window: those must not be read.)
             if (lane < kRowsPerWarp) sm->valid[g][my_row] = 1;
             if (warp == 0 && lane == 0) {
-#pragma unroll
+#pragma unroll 1
               for (int i = 0; i < kParts; ++i) {
                 const int b0 = 4 * i, b1 = min(NB, b0 + 4);
                 tc::mbar_arrive_expect_tx(&sm->kv_full[g][i], (b1 - b0) * kBoxBytes);
+#pragma unroll 1
                 for (int bx = b0; bx < b1; ++bx)
                   tc::tma_load_2d(kv + g * kTileBytes + bx * kBoxBytes, &tm_win, 64 * bx, L.b * a.T_raw + L.wlo + r0,
                                   &sm->kv_full[g][i]);
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t code_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.pages) + (uint64_t)at * (kD / 2) : 0;
         const uint64_t scale_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.scales) + (uint64_t)at * (kD / 16) : 0;
         constexpr int kPer = 2 * NB;  // 16-byte pieces of a row's codes
-#pragma unroll 2
+#pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int n = 32 * i + lane, rw = n / kPer, c = n - rw * kPer;
           const uint64_t row = __shfl_sync(0xffffffffu, code_row, rw);
@@ -660,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (done > 0 && !(ok = ready(&sm->q_empty, (done - 1) & 1))) break;
       if (tc::elect_one()) {
         tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
+#pragma unroll 1
         for (int bx = 0; bx < NB; ++bx) tc::tma_load_3d(qs + bx * kQBoxBytes, &tm_q, bx * 64, it.h0, it.qq, &sm->q_full);
       }
       __syncwarp();
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mo = sm->mref[h];
           const bool first = mo == kFloor, up = first ? tm != -INFINITY : tm > kRescaleLog2;
           if (up) sm->mref[h] = first ? tm : mo + tm;
-          sm->alpha[h] = up && !first ? exp2f(-tm) : 1.f;
+          sm->alpha[h] = up && !first ? ex2_approx(-tm) : 1.f;
           const bool any = __any_sync(0xffffffffu, up && !first);
           if (lane == 0) sm->rescale[half] = any ? 1 : 0;
         }
@@ -896,8 +898,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (splits > 1) {
           reinterpret_cast<float2 *>(a.part_ml)[((size_t)it.qq * a.H + it.h0 + h) * splits + split] = make_float2(mr, ls);
         } else {  // fold in the sink (logit sink[h], value 0) and normalise
-          const float sk = a.sink[it.h0 + h] * kLog2e, M = fmaxf(mr, sk), wm = exp2f(mr - M);
-          const float Ls = ls * wm + exp2f(sk - M);
+          const float sk = a.sink[it.h0 + h] * kLog2e, M = fmaxf(mr, sk), wm = ex2_approx(mr - M);
+          const float Ls = ls * wm + ex2_approx(sk - M);
           sm->norm[h] = Ls == 0.f ? 0.f : wm / Ls;
         }
       }
