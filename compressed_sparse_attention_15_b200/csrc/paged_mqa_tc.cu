@@ -12,10 +12,11 @@
 // widen8) on its way into shared memory. A lane takes 32 bytes of a row, the 64 dims of one
 // 128-byte swizzled line, and 8 lanes take 8 rows, so that every 16-byte store
 // of theirs falls into distinct banks. The packed rows come through a staging
-// tile, which two warps fill by asynchronous copies while the tile before is
-// widened: loads into registers would have to be waited for at the fence that
-// shows a tile to the tensor core. Their lookups (list, page table) run three
-// tiles ahead, each load a tile ahead of its use.
+// tile: each warp copies its own rows of the next tile there, asynchronously, once
+// it has read those of the current one into registers (loads into registers would
+// have to be waited for at the fence that shows a tile to the tensor core). Two
+// warps look the rows up (list, page table), each load a tile ahead of its use, and
+// publish them two tiles ahead.
 //
 // Two tiles are in flight (a third does not fit beside the queries), so a
 // tile's way through widening, S^T, softmax and P.V bounds the rate as much as
@@ -68,7 +69,7 @@ struct Small {
   // per tile buffer (and half of the dims): filled, read; per tile buffer: S^T made, P^T written
   uint64_t kv_full[2][2], kv_empty[2][2], s_full[2];
   uint64_t p_full;                             // P^T written
-  uint64_t stage_full, stage_empty;            // the staging tile and its slots: filled, read
+  uint64_t slot_full[2], slot_empty[2];        // a tile's slots: published, read
   uint64_t pv_done[4];                         // P.V made, per tile (mod 4)
   uint64_t q_full, q_empty, o_done, o_free;    // per item: queries loaded / read, O^T made / read
   uint64_t norm_full;                          // per item: norm is there
@@ -83,7 +84,7 @@ struct Small {
   int abort;
   int rescale[2];             // per half of the heads
   uint8_t valid[2][kRows];    // per tile buffer: the row holds a key
-  long long slot[kRows];      // of the staged tile: row of the window or of the pages, -1: no key
+  long long slot[2][kRows];   // of a tile (mod 2): row of the window or of the pages, -1: no key
 };
 
 // The staging tile: 64 rows of codes, then of scales. Row strides that put 8
@@ -205,11 +206,6 @@ __device__ __forceinline__ void copy_piece(uint32_t dst, uint64_t src) {
         "{\n\t.reg .pred p;\n\tsetp.ne.u64 p, %1, 0;\n\t"
         "@p cp.async.ca.shared.global [%0], [%1], 8;\n\t@!p st.shared.v2.b32 [%0], {%2, %2};\n\t}" ::"r"(dst), "l"(src), "r"(0)
         : "memory");
-}
-
-// An arrival on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
 // *p, or 0 without reading it where !pred. (One predicated load: no branch at
@@ -400,8 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sm->s_full[i], 1);
     }
     tc::mbar_init(&sm->p_full, 32 * kSoftWarps);
-    tc::mbar_init(&sm->stage_full, 2 * kRows);  // each fetching lane arrives, and so do its copies
-    tc::mbar_init(&sm->stage_empty, kLoadWarps);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm->slot_full[i], kRows);
+      tc::mbar_init(&sm->slot_empty[i], kLoadWarps);
+    }
     for (int i = 0; i < 4; ++i) tc::mbar_init(&sm->pv_done[i], 1);
     tc::mbar_init(&sm->q_full, 1);
     tc::mbar_init(&sm->q_empty, 1);
@@ -456,16 +454,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item L;
       ok = take_item(a, sm, k, abort, L);
       if (!ok || L.qv < 0) break;
+      // This warp's rows of tile li: their slots, and their packed bytes on their way into the staging tile.
+      long long next_slot = -1;
+      auto stage_rows = [&](int li, uint32_t t) {
+        ok = ok && warp_wait(&sm->slot_full[t & 1], (t >> 1) & 1, abort, a.status);
+        if (!ok) return;
+        next_slot = sm->slot[t & 1][my_row];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm->slot_empty[t & 1]);
+        if (kInt4 && (L.t0 + li) * kRows >= L.w64) {
+          // this lane's row as an address (0: no key); every lane copies pieces of every row
+          const uint64_t code_row = next_slot >= 0 ? reinterpret_cast<uint64_t>(a.cache.pages) + (uint64_t)next_slot * (kD / 2) : 0;
+          const uint64_t scale_row = next_slot >= 0 ? reinterpret_cast<uint64_t>(a.cache.scales) + (uint64_t)next_slot * (kD / 16) : 0;
+          constexpr int kPer = 2 * NB;  // 16-byte pieces of a row's codes
+#pragma unroll
+          for (int i = 0; i < kRowsPerWarp * kPer / 32; ++i) {
+            const int n = 32 * i + lane, rw = n / kPer, c = n - rw * kPer;
+            const uint64_t row = __shfl_sync(0xffffffffu, code_row, rw);
+            copy_piece<16>(stage_base + (kRowsPerWarp * warp + rw) * stage_row(NB) + 16 * c, row ? row + 16 * c : 0);
+          }
+          constexpr int kPiece = NB % 4 ? 8 : 16, kPerS = 4 * NB / kPiece;  // pieces of a row's scales
+          const int rw = lane / kPerS, c = lane - rw * kPerS;
+          const uint64_t row = __shfl_sync(0xffffffffu, scale_row, rw & 7);
+          if (rw < kRowsPerWarp)
+            copy_piece<kPiece>(stage_base + kRows * stage_row(NB) + (kRowsPerWarp * warp + rw) * kStageScaleRow + kPiece * c,
+                               row ? row + kPiece * c : 0);
+        }
+      };
+      if (L.ntiles > 0) stage_rows(0, T);
       for (int li = 0; li < L.ntiles; ++li, ++T) {
         const int g = T & 1;
         if (out_qv >= 0 && T == out_at) output();
         if (!ok) break;
         const uint32_t free_phase = ((T >> 1) & 1) ^ 1, line = kv_base + g * kTileBytes + my_row * 128 + ((lane & 7) << 4);
         const bool in_win = (L.t0 + li) * kRows < L.w64;
-        ok = warp_wait(&sm->stage_full, T & 1, abort, a.status);
-        if (!ok) break;
-        const long long slot = sm->slot[my_row];
+        const long long slot = next_slot;
         if (kInt4 && !in_win) {
+          cp_async_wait_all();
+          __syncwarp();
           Packed u[kParts];
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
@@ -473,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_packed(u[i], codes + 32 * s, scales + 4 * s);
           }
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm->stage_empty);
+          if (li + 1 < L.ntiles) stage_rows(li + 1, T + 1);
+          if (!ok) break;
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
             ok = warp_wait(&sm->kv_empty[g][i], free_phase, abort, a.status);
@@ -485,8 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_arrive(&sm->kv_full[g][i]);
           }
         } else {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm->stage_empty);
+          if (li + 1 < L.ntiles) stage_rows(li + 1, T + 1);
 #pragma unroll
           for (int i = 0; i < kParts; ++i)
             ok = ok && wait(&sm->kv_empty[g][i], free_phase, abort, a.status);
@@ -539,14 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (out_qv >= 0) output();
+    cp_async_wait_all();
     if (!ok && tma_last >= 0)  // (nothing is in flight when the block ends; without a fault every tile was used)
 #pragma unroll
       for (int i = 0; i < kParts; ++i) tc::mbar_drain(&sm->kv_full[tma_last & 1][i], (tma_last >> 1) & 1);
   } else if (warp >= kFetchWarp0) {
-    // ------------------------------------------------------------ lookups and fetches
-    // A lane looks one row up; a warp copies its 32 rows.
-    const int half = warp - kFetchWarp0, my_row = 32 * half + lane;
-    const uint32_t codes = tc::smem_u32(stage), scales = codes + kRows * stage_row(NB);
+    // ------------------------------------------------------------ lookups
+    // A lane looks one row up.
+    const int my_row = 32 * (warp - kFetchWarp0) + lane;
     uint32_t T = 0;
     bool ok = true;
     // The first of these warps also makes the block's items, the next when it has
@@ -612,40 +638,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     int2 p1 = page_of(1, e1);
     long long at = row_of(0, p0);
     for (int li = 0; li < ntiles; ++li, ++T) {
-      ok = warp_wait(&sm->stage_empty, (T & 1) ^ 1, abort, a.status);
+      ok = warp_wait(&sm->slot_empty[T & 1], ((T >> 1) & 1) ^ 1, abort, a.status);
       if (!ok) break;
-      sm->slot[my_row] = at;
-      if (kInt4 && !is_win(li)) {
-        // this lane's row as an address (0: no key); every lane copies pieces of every row
-        const uint64_t code_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.pages) + (uint64_t)at * (kD / 2) : 0;
-        const uint64_t scale_row = at >= 0 ? reinterpret_cast<uint64_t>(a.cache.scales) + (uint64_t)at * (kD / 16) : 0;
-        constexpr int kPer = 2 * NB;  // 16-byte pieces of a row's codes
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int n = 32 * i + lane, rw = n / kPer, c = n - rw * kPer;
-          const uint64_t row = __shfl_sync(0xffffffffu, code_row, rw);
-          copy_piece<16>(codes + (32 * half + rw) * stage_row(NB) + 16 * c, row ? row + 16 * c : 0);
-        }
-        constexpr int kPiece = NB % 4 ? 8 : 16, kPerS = 4 * NB / kPiece;  // pieces of a row's scales
-#pragma unroll
-        for (int i = 0; i < kPerS; ++i) {
-          const int n = 32 * i + lane, rw = n / kPerS, c = n - rw * kPerS;
-          const uint64_t row = __shfl_sync(0xffffffffu, scale_row, rw);
-          copy_piece<kPiece>(scales + (32 * half + rw) * kStageScaleRow + kPiece * c, row ? row + kPiece * c : 0);
-        }
-      } else if (at >= 0) {  // a bf16 row: into L2, for the copy
+      sm->slot[T & 1][my_row] = at;
+      if ((!kInt4 || is_win(li)) && at >= 0) {  // a bf16 row: into L2, for the copy
         const bf16 *base = is_win(li) ? static_cast<const bf16 *>(a.kv_win) + (size_t)b * a.T_raw * kD
                                       : reinterpret_cast<const bf16 *>(a.cache.pages);
         bulk_prefetch_l2(base + (size_t)at * kD, kD * 2);
       }
-      cp_async_arrive(&sm->stage_full);
-      tc::mbar_arrive(&sm->stage_full);
+      tc::mbar_arrive(&sm->slot_full[T & 1]);
       at = row_of(li + 1, p1);
       p1 = page_of(li + 2, e2);
       e2 = entry_of(li + 3);
     }
     }
-    cp_async_wait_all();  // (nothing is in flight when the block ends)
   } else if (warp == kSWarp) {
     // ------------------------------------------------------------ queries, S^T
     // (the whole warp runs the loops of the two issuers; one lane issues)
