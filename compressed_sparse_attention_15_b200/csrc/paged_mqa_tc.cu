@@ -72,14 +72,16 @@ struct Small {
   uint64_t slot_full[2], slot_empty[2];        // a tile's slots: published, read
   uint64_t pv_done[4];                         // P.V made, per tile (mod 4)
   uint64_t q_full, q_empty, o_done, o_free;    // per item: queries loaded / read, O^T made / read
-  uint64_t norm_full;                          // per item: norm is there
+  uint64_t norm_full[2];                       // per item (mod 2): norm is there
   uint64_t s_fin, pv_fin;                      // the last products of the block
   uint64_t item_full[4], item_empty[4];        // ring of the block's items
   alignas(16) int item[4][8];                  // of struct Item: qv, t0, ntiles, b, nsel, wlo, nwin, w64
   float red[4][kH];
   float mref[kH];
   float alpha[kH];            // what a rescale multiplies by
-  float norm[kH];             // what the item's output is multiplied by
+  // What an item's output is multiplied by: of its items with tiles in turn, and of
+  // one without (an item of one tile gets there before the one before it is written).
+  float norm[3][kH];
   uint32_t tmem_base;
   int abort;
   int rescale[2];             // per half of the heads
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&sm->q_empty, 1);
     tc::mbar_init(&sm->o_done, 1);
     tc::mbar_init(&sm->o_free, 32 * (kLoadWarps + kSoftWarps));
-    tc::mbar_init(&sm->norm_full, kH);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm->norm_full[i], kH);
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sm->item_full[i], 1);
       tc::mbar_init(&sm->item_empty[i], kThreads / 32);
@@ -439,13 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int out_qv = -1;
     uint32_t out_at = 0, done = 0;  // the tile before which it is written; items written
     auto output = [&] {
-      ok = ok && wait(&sm->norm_full, done & 1, abort, a.status);
+      ok = ok && wait(&sm->norm_full[done & 1], (done >> 1) & 1, abort, a.status);
       ok = ok && wait(&sm->o_done, done & 1, abort, a.status);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
       const int half = warp >> 2, h0 = (a.H > kH ? (out_qv & 1) * kH : 0) + 32 * half;
       if (ok)
-        write_out<NB>(a, tmem + 32 * half, sm->norm + 32 * half, (size_t)query_of(a, out_qv) * a.H + h0, a.H - h0, warp & 3,
+        write_out<NB>(a, tmem + 32 * half, sm->norm[done & 1] + 32 * half, (size_t)query_of(a, out_qv) * a.H + h0, a.H - h0, warp & 3,
                       NB / 2, NB, true, &sm->o_free);
       ++done;
       out_qv = -1;
@@ -580,77 +582,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     // claim and the loads take, and the blocks end as evenly as may be.
     const bool maker = warp == kFetchWarp0;
     for (uint32_t k = 0; ok; ++k) {
-    if (maker) {
-      int next = blockIdx.x;  // (the first item is the block's own)
-      if (k > 0) {
-        next = qvs;
-        if (qvs > (int)gridDim.x) next = __shfl_sync(0xffffffffu, lane == 0 ? (int)(gridDim.x + atomicAdd(a.status + 4, 1u)) : 0, 0);
+      if (maker) {
+        int next = blockIdx.x;  // (the first item is the block's own)
+        if (k > 0) {
+          next = qvs;
+          if (qvs > (int)gridDim.x) next = __shfl_sync(0xffffffffu, lane == 0 ? (int)(gridDim.x + atomicAdd(a.status + 4, 1u)) : 0, 0);
+        }
+        const int3 v = next < qvs ? item_rows(a, next, lane, blockIdx.y == 0 && lane == 0 ? a.status : nullptr) : make_int3(0, 0, 0);
+        ok = warp_wait(&sm->item_empty[k & 3], ((k >> 2) & 1) ^ 1, abort, a.status);
+        if (ok && lane == 0) {
+          const int w64 = (v.z + kRows - 1) / kRows * kRows, tiles = (w64 + v.x + kRows - 1) / kRows;
+          const int splits = gridDim.y, split = blockIdx.y, base = tiles / splits, rest = tiles - base * splits;
+          *reinterpret_cast<int4 *>(sm->item[k & 3]) = make_int4(next < qvs ? next : -1, split * base + min(split, rest),
+                                                                 base + (split < rest ? 1 : 0), query_of(a, next) / a.q_per_seq);
+          *reinterpret_cast<int4 *>(sm->item[k & 3] + 4) = make_int4(v.x, v.y, v.z, w64);
+          tc::mbar_arrive(&sm->item_full[k & 3]);
+        }
       }
-      const int3 v = next < qvs ? item_rows(a, next, lane, blockIdx.y == 0 && lane == 0 ? a.status : nullptr) : make_int3(0, 0, 0);
-      ok = warp_wait(&sm->item_empty[k & 3], ((k >> 2) & 1) ^ 1, abort, a.status);
-      if (lane == 0) {
-        const int w64 = (v.z + kRows - 1) / kRows * kRows, tiles = (w64 + v.x + kRows - 1) / kRows;
-        const int splits = gridDim.y, split = blockIdx.y, base = tiles / splits, rest = tiles - base * splits;
-        *reinterpret_cast<int4 *>(sm->item[k & 3]) = make_int4(next < qvs ? next : -1, split * base + min(split, rest),
-                                                               base + (split < rest ? 1 : 0), query_of(a, next) / a.q_per_seq);
-        *reinterpret_cast<int4 *>(sm->item[k & 3] + 4) = make_int4(v.x, v.y, v.z, w64);
-        tc::mbar_arrive(&sm->item_full[k & 3]);
+      Item L;
+      ok = take_item(a, sm, k, abort, L);
+      if (!ok || L.qv < 0) break;
+      const int t0 = L.t0, ntiles = L.ntiles, b = L.b, qq = L.qq;
+      auto is_win = [&](int li) { return (t0 + li) * kRows < L.w64; };
+      // The lookup of this lane's row of tile li in three steps, each one load: the
+      // row's entry, or number in the window; ...
+      struct Entry {
+        int j;
+        bool live;
+      };
+      auto entry_of = [&](int li) -> Entry {
+        const int r = (t0 + li) * kRows + my_row, p = r - L.w64;
+        const bool mine = li < ntiles;
+        if (p < 0) return Entry{L.wlo + r, mine && r < L.nwin};
+        const bool live = mine && p < L.nsel;
+        return Entry{a.idx ? load_if(a.idx + (size_t)qq * a.k + p, live) : p, live};
+      };
+      // ... its page and the row there (-1: no key); ...
+      auto page_of = [&](int li, Entry e) -> int2 {
+        if (is_win(li)) return make_int2(0, e.live ? e.j : -1);
+        const bool ok = e.live && e.j >= 0 && e.j < a.cache.capacity();
+        if (e.live && !ok && e.j != -1) raise_status(a.status, CSA_STATUS_BAD_INDEX);
+        const uint2 at = page_and_row(a.cache, ok ? e.j : 0);
+        return make_int2(load_if(a.cache.table + (size_t)b * a.cache.per + at.x, ok), ok ? (int)at.y : -1);
+      };
+      // ... and the row of the window or of the pages.
+      auto row_of = [&](int li, int2 pg) -> long long {
+        if (pg.y < 0 || is_win(li)) return pg.y;
+        if (pg.x < 0 || pg.x >= a.cache.num_pages) {
+          raise_status(a.status, CSA_STATUS_BAD_PAGE);
+          return -1;
+        }
+        return (long long)pg.x * a.cache.page + pg.y;
+      };
+      const Entry e0 = entry_of(0), e1 = entry_of(1);
+      Entry e2 = entry_of(2);
+      const int2 p0 = page_of(0, e0);
+      int2 p1 = page_of(1, e1);
+      long long at = row_of(0, p0);
+      for (int li = 0; li < ntiles; ++li, ++T) {
+        ok = warp_wait(&sm->slot_empty[T & 1], ((T >> 1) & 1) ^ 1, abort, a.status);
+        if (!ok) break;
+        sm->slot[T & 1][my_row] = at;
+        if ((!kInt4 || is_win(li)) && at >= 0) {  // a bf16 row: into L2, for the copy
+          const bf16 *base = is_win(li) ? static_cast<const bf16 *>(a.kv_win) + (size_t)b * a.T_raw * kD
+                                        : reinterpret_cast<const bf16 *>(a.cache.pages);
+          bulk_prefetch_l2(base + (size_t)at * kD, kD * 2);
+        }
+        tc::mbar_arrive(&sm->slot_full[T & 1]);
+        at = row_of(li + 1, p1);
+        p1 = page_of(li + 2, e2);
+        e2 = entry_of(li + 3);
       }
-    }
-    Item L;
-    ok = take_item(a, sm, k, abort, L);
-    if (!ok || L.qv < 0) break;
-    const int t0 = L.t0, ntiles = L.ntiles, b = L.b, qq = L.qq;
-    auto is_win = [&](int li) { return (t0 + li) * kRows < L.w64; };
-    // The lookup of this lane's row of tile li in three steps, each one load: the
-    // row's entry, or number in the window; ...
-    struct Entry {
-      int j;
-      bool live;
-    };
-    auto entry_of = [&](int li) -> Entry {
-      const int r = (t0 + li) * kRows + my_row, p = r - L.w64;
-      const bool mine = li < ntiles;
-      if (p < 0) return Entry{L.wlo + r, mine && r < L.nwin};
-      const bool live = mine && p < L.nsel;
-      return Entry{a.idx ? load_if(a.idx + (size_t)qq * a.k + p, live) : p, live};
-    };
-    // ... its page and the row there (-1: no key); ...
-    auto page_of = [&](int li, Entry e) -> int2 {
-      if (is_win(li)) return make_int2(0, e.live ? e.j : -1);
-      const bool ok = e.live && e.j >= 0 && e.j < a.cache.capacity();
-      if (e.live && !ok && e.j != -1) raise_status(a.status, CSA_STATUS_BAD_INDEX);
-      const uint2 at = page_and_row(a.cache, ok ? e.j : 0);
-      return make_int2(load_if(a.cache.table + (size_t)b * a.cache.per + at.x, ok), ok ? (int)at.y : -1);
-    };
-    // ... and the row of the window or of the pages.
-    auto row_of = [&](int li, int2 pg) -> long long {
-      if (pg.y < 0 || is_win(li)) return pg.y;
-      if (pg.x < 0 || pg.x >= a.cache.num_pages) {
-        raise_status(a.status, CSA_STATUS_BAD_PAGE);
-        return -1;
-      }
-      return (long long)pg.x * a.cache.page + pg.y;
-    };
-    const Entry e0 = entry_of(0), e1 = entry_of(1);
-    Entry e2 = entry_of(2);
-    const int2 p0 = page_of(0, e0);
-    int2 p1 = page_of(1, e1);
-    long long at = row_of(0, p0);
-    for (int li = 0; li < ntiles; ++li, ++T) {
-      ok = warp_wait(&sm->slot_empty[T & 1], ((T >> 1) & 1) ^ 1, abort, a.status);
-      if (!ok) break;
-      sm->slot[T & 1][my_row] = at;
-      if ((!kInt4 || is_win(li)) && at >= 0) {  // a bf16 row: into L2, for the copy
-        const bf16 *base = is_win(li) ? static_cast<const bf16 *>(a.kv_win) + (size_t)b * a.T_raw * kD
-                                      : reinterpret_cast<const bf16 *>(a.cache.pages);
-        bulk_prefetch_l2(base + (size_t)at * kD, kD * 2);
-      }
-      tc::mbar_arrive(&sm->slot_full[T & 1]);
-      at = row_of(li + 1, p1);
-      p1 = page_of(li + 2, e2);
-      e2 = entry_of(li + 3);
-    }
     }
   } else if (warp == kSWarp) {
     // ------------------------------------------------------------ queries, S^T
@@ -756,173 +758,179 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t T = 0, done = 0;  // tiles so far, items with tiles so far
     const int splits = gridDim.y, split = blockIdx.y;
-    for (uint32_t k = 0; ok; ++k) {
-    Item it;
-    ok = take_item(a, sm, k, abort, it);
-    if (!ok || it.qv < 0) break;
-    const int nh = min(kH, a.H - it.h0);
-    uint64_t nm[4], l[4];  // per pair of heads: minus the reference (of log2 logits), the running sum
-    bool fresh = true;     // some of this thread's heads have had no row
+    for (uint32_t k = 0;; ++k) {
+      Item it;
+      ok = ok && take_item(a, sm, k, abort, it);
+      // (the warps of a half leave together: whoever stays waits for the others at the barriers below)
+      if (bar_any(1 + half, 128, !ok)) {
+        ok = false;
+        break;
+      }
+      if (it.qv < 0) break;
+      const int nh = min(kH, a.H - it.h0);
+      uint64_t nm[4], l[4];  // per pair of heads: minus the reference (of log2 logits), the running sum
+      bool fresh = true;     // some of this thread's heads have had no row
 #pragma unroll
-    for (int c = 0; c < 4; ++c) nm[c] = l[c] = pack2(0.f, 0.f);
-    for (int li = 0; li < it.ntiles; ++li, ++T) {
-      const int buf = T & 1;
-      // (kv_full too: the row flags are the loaders' own writes)
-      bool got = wait(&sm->kv_full[buf][0], (T >> 1) & 1, abort, a.status);
-      got = got && wait(&sm->s_full[buf], (T >> 1) & 1, abort, a.status);
-      got = __all_sync(0xffffffffu, got);
-      tc::fence_after_sync();
-      const bool validA = sm->valid[buf][rowA], validB = sm->valid[buf][rowB];
-      const bool full = __all_sync(0xffffffffu, validA && validB);
-      uint32_t v[16];
-      tmem_ld_16x256b_x4(tmem + lane_off + kColS + 64 * buf + 32 * half, v);
-      tc::tmem_ld_wait();
-      // y = logit - reference, in log2 units; rows without a key are -inf. A
-      // head's reference moves only when some logit of a tile exceeds it by more
-      // than 2^8, and on its first row (it is 0 until then, and not final).
-      float2 yA[4], yB[4];
-      bool rescale = false;
+      for (int c = 0; c < 4; ++c) nm[c] = l[c] = pack2(0.f, 0.f);
+      for (int li = 0; li < it.ntiles; ++li, ++T) {
+        const int buf = T & 1;
+        // (kv_full too: the row flags are the loaders' own writes)
+        bool got = wait(&sm->kv_full[buf][0], (T >> 1) & 1, abort, a.status);
+        got = got && wait(&sm->s_full[buf], (T >> 1) & 1, abort, a.status);
+        got = __all_sync(0xffffffffu, got);
+        tc::fence_after_sync();
+        const bool validA = sm->valid[buf][rowA], validB = sm->valid[buf][rowB];
+        const bool full = __all_sync(0xffffffffu, validA && validB);
+        uint32_t v[16];
+        tmem_ld_16x256b_x4(tmem + lane_off + kColS + 64 * buf + 32 * half, v);
+        tc::tmem_ld_wait();
+        // y = logit - reference, in log2 units; rows without a key are -inf. A
+        // head's reference moves only when some logit of a tile exceeds it by more
+        // than 2^8, and on its first row (it is 0 until then, and not final).
+        float2 yA[4], yB[4];
+        bool rescale = false;
 #pragma unroll 1
-      for (int pass = 0;; ++pass) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          yA[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), scale2, nm[c]));
-          yB[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), scale2, nm[c]));
-        }
-        if (!full) {
+        for (int pass = 0;; ++pass) {
+          float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (!validA) yA[c] = make_float2(-INFINITY, -INFINITY);
-            if (!validB) yB[c] = make_float2(-INFINITY, -INFINITY);
+            yA[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), scale2, nm[c]));
+            yB[c] = unpack2(fma2(pack2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), scale2, nm[c]));
+          }
+          if (!full) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (!validA) yA[c] = make_float2(-INFINITY, -INFINITY);
+              if (!validB) yB[c] = make_float2(-INFINITY, -INFINITY);
+            }
+          }
+          if (pass) break;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top = fmaxf(fmaxf(top, fmaxf(yA[c].x, yA[c].y)), fmaxf(yB[c].x, yB[c].y));
+          if (!bar_any(1 + half, 128, top > kRescaleLog2 || fresh || !(got && ok))) break;
+          if (bar_any(1 + half, 128, !(got && ok))) {  // S^T(li) missing, or the previous P.V never completed
+            ok = false;
+            break;
+          }
+          // per-head tile maximum: over the thread's two rows, then over the 8
+          // lanes of the same cq, then over the 4 warps
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float2 mx = make_float2(fmaxf(yA[c].x, yB[c].x), fmaxf(yA[c].y, yB[c].y));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+              mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+            }
+            if (rq == 0) *reinterpret_cast<float2 *>(red + 8 * c + 2 * cq) = mx;
+          }
+          named_sync(1 + half, 128);
+          if (quarter == 0) {
+            const int h = 32 * half + lane;
+            const float tm = fmaxf(fmaxf(sm->red[0][h], sm->red[1][h]), fmaxf(sm->red[2][h], sm->red[3][h]));
+            const float mo = sm->mref[h];
+            const bool first = mo == kFloor, up = first ? tm != -INFINITY : tm > kRescaleLog2;
+            if (up) sm->mref[h] = first ? tm : mo + tm;
+            sm->alpha[h] = up && !first ? ex2_approx(-tm) : 1.f;
+            const bool any = __any_sync(0xffffffffu, up && !first);
+            if (lane == 0) sm->rescale[half] = any ? 1 : 0;
+          }
+          named_sync(1 + half, 128);
+          rescale = sm->rescale[half] != 0;
+          fresh = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 m = *reinterpret_cast<const float2 *>(&sm->mref[32 * half + 8 * c + 2 * cq]);
+            fresh |= m.x == kFloor || m.y == kFloor;
+            nm[c] = pack2(m.x == kFloor ? 0.f : -m.x, m.y == kFloor ? 0.f : -m.y);
+            if (rescale) {
+              const float2 al = *reinterpret_cast<const float2 *>(&sm->alpha[32 * half + 8 * c + 2 * cq]);
+              l[c] = mul2(l[c], pack2(al.x, al.y));
+            }
           }
         }
-        if (pass) break;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) top = fmaxf(fmaxf(top, fmaxf(yA[c].x, yA[c].y)), fmaxf(yB[c].x, yB[c].y));
-        if (!bar_any(1 + half, 128, top > kRescaleLog2 || fresh || !(got && ok))) break;
-        if (bar_any(1 + half, 128, !(got && ok))) {  // S^T(li) missing, or the previous P.V never completed
-          ok = false;
-          break;
-        }
-        // per-head tile maximum: over the thread's two rows, then over the 8
-        // lanes of the same cq, then over the 4 warps
+        if (!ok) break;
+        // P = 2^y, rounded to bf16 and summed per head. The sums take the same
+        // bf16 weights as P.V, so that a dominant row's weight (up to 2^8 between
+        // rescales) cancels exactly.
+        uint32_t pA[4], pB[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float2 mx = make_float2(fmaxf(yA[c].x, yB[c].x), fmaxf(yA[c].y, yB[c].y));
+          const __nv_bfloat162 ta = __floats2bfloat162_rn(ex2_approx(yA[c].x), ex2_approx(yA[c].y));
+          const __nv_bfloat162 tb = __floats2bfloat162_rn(ex2_approx(yB[c].x), ex2_approx(yB[c].y));
+          pA[c] = *reinterpret_cast<const uint32_t *>(&ta);
+          pB[c] = *reinterpret_cast<const uint32_t *>(&tb);
+          l[c] = add2(l[c], pack2(__uint_as_float(pA[c] << 16), __uint_as_float(pA[c] & 0xffff0000u)));
+          l[c] = add2(l[c], pack2(__uint_as_float(pB[c] << 16), __uint_as_float(pB[c] & 0xffff0000u)));
+        }
+        // P.V of the tile before has to be complete before P^T, and where the
+        // maximum moved O^T too, are written again.
+        if (T > 0) {
+          ok = warp_wait(&sm->pv_done[(T - 1) & 3], ((T - 1) >> 2) & 1, abort, a.status);
+          tc::fence_after_sync();
+        }
+        stmatrix_x4(pdst, pA[0], pB[0], pA[1], pB[1]);
+        stmatrix_x4(pdst ^ 32, pA[2], pB[2], pA[3], pB[3]);
+        if (li > 0 && rescale) {
+          if (ok) {
+#pragma unroll 1
+            for (int m = 0; m < NB; ++m) {  // 16 heads of a 128-dim chunk at a time
+              const int h = 32 * half + 16 * (m & 1);
+              uint32_t o[16];
+              const uint32_t ta = tmem + lane_off + 64 * (m >> 1) + h;
+              tmem_ld16(ta, o);
+              tc::tmem_ld_wait();
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
-            mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
-          }
-          if (rq == 0) *reinterpret_cast<float2 *>(red + 8 * c + 2 * cq) = mx;
-        }
-        named_sync(1 + half, 128);
-        if (quarter == 0) {
-          const int h = 32 * half + lane;
-          const float tm = fmaxf(fmaxf(sm->red[0][h], sm->red[1][h]), fmaxf(sm->red[2][h], sm->red[3][h]));
-          const float mo = sm->mref[h];
-          const bool first = mo == kFloor, up = first ? tm != -INFINITY : tm > kRescaleLog2;
-          if (up) sm->mref[h] = first ? tm : mo + tm;
-          sm->alpha[h] = up && !first ? ex2_approx(-tm) : 1.f;
-          const bool any = __any_sync(0xffffffffu, up && !first);
-          if (lane == 0) sm->rescale[half] = any ? 1 : 0;
-        }
-        named_sync(1 + half, 128);
-        rescale = sm->rescale[half] != 0;
-        fresh = false;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 m = *reinterpret_cast<const float2 *>(&sm->mref[32 * half + 8 * c + 2 * cq]);
-          fresh |= m.x == kFloor || m.y == kFloor;
-          nm[c] = pack2(m.x == kFloor ? 0.f : -m.x, m.y == kFloor ? 0.f : -m.y);
-          if (rescale) {
-            const float2 al = *reinterpret_cast<const float2 *>(&sm->alpha[32 * half + 8 * c + 2 * cq]);
-            l[c] = mul2(l[c], pack2(al.x, al.y));
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * sm->alpha[h + c]);
+              tmem_st16(ta, o);
+            }
+            tmem_st_wait();
           }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc::fence_before_sync();
+        tc::mbar_arrive(&sm->p_full);
       }
-      if (!ok) break;
-      // P = 2^y, rounded to bf16 and summed per head. The sums take the same
-      // bf16 weights as P.V, so that a dominant row's weight (up to 2^8 between
-      // rescales) cancels exactly.
-      uint32_t pA[4], pB[4];
+      // Per-head sums, and what the output is multiplied by.
+      const int which = it.ntiles > 0 ? done & 1 : 2;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const __nv_bfloat162 ta = __floats2bfloat162_rn(ex2_approx(yA[c].x), ex2_approx(yA[c].y));
-        const __nv_bfloat162 tb = __floats2bfloat162_rn(ex2_approx(yB[c].x), ex2_approx(yB[c].y));
-        pA[c] = *reinterpret_cast<const uint32_t *>(&ta);
-        pB[c] = *reinterpret_cast<const uint32_t *>(&tb);
-        l[c] = add2(l[c], pack2(__uint_as_float(pA[c] << 16), __uint_as_float(pA[c] & 0xffff0000u)));
-        l[c] = add2(l[c], pack2(__uint_as_float(pB[c] << 16), __uint_as_float(pB[c] & 0xffff0000u)));
-      }
-      // P.V of the tile before has to be complete before P^T, and where the
-      // maximum moved O^T too, are written again.
-      if (T > 0) {
-        ok = warp_wait(&sm->pv_done[(T - 1) & 3], ((T - 1) >> 2) & 1, abort, a.status);
-        tc::fence_after_sync();
-      }
-      stmatrix_x4(pdst, pA[0], pB[0], pA[1], pB[1]);
-      stmatrix_x4(pdst ^ 32, pA[2], pB[2], pA[3], pB[3]);
-      if (li > 0 && rescale) {
-        if (ok) {
-#pragma unroll 1
-          for (int m = 0; m < NB; ++m) {  // 16 heads of a 128-dim chunk at a time
-            const int h = 32 * half + 16 * (m & 1);
-            uint32_t o[16];
-            const uint32_t ta = tmem + lane_off + 64 * (m >> 1) + h;
-            tmem_ld16(ta, o);
-            tc::tmem_ld_wait();
+        float2 s = unpack2(l[c]);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * sm->alpha[h + c]);
-            tmem_st16(ta, o);
+        for (int o = 4; o < 32; o <<= 1) {
+          s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+          s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+        }
+        if (rq == 0) *reinterpret_cast<float2 *>(red + 8 * c + 2 * cq) = s;
+      }
+      named_sync(1 + half, 128);
+      if (quarter == 0) {
+        const int h = 32 * half + lane;
+        const float ls = (sm->red[0][h] + sm->red[1][h]) + (sm->red[2][h] + sm->red[3][h]);
+        const float mr = sm->mref[h];
+        if (h < nh) {
+          if (splits > 1) {
+            reinterpret_cast<float2 *>(a.part_ml)[((size_t)it.qq * a.H + it.h0 + h) * splits + split] = make_float2(mr, ls);
+          } else {  // fold in the sink (logit sink[h], value 0) and normalise
+            const float sk = a.sink[it.h0 + h] * kLog2e, M = fmaxf(mr, sk), wm = ex2_approx(mr - M);
+            const float Ls = ls * wm + ex2_approx(sk - M);
+            sm->norm[which][h] = Ls == 0.f ? 0.f : wm / Ls;
           }
-          tmem_st_wait();
         }
+        sm->mref[h] = kFloor;  // for the next item, which reads it after a barrier
+        if (it.ntiles > 0) tc::mbar_arrive(&sm->norm_full[done & 1]);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      tc::fence_before_sync();
-      tc::mbar_arrive(&sm->p_full);
-    }
-    // Per-head sums, and what the output is multiplied by.
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float2 s = unpack2(l[c]);
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+      named_sync(1 + half, 128);
+      // These warps' half of the output (all of it where the item has no tiles).
+      const bool some = it.ntiles > 0;
+      if (some) {
+        ok = __all_sync(0xffffffffu, ok && wait(&sm->o_done, done & 1, abort, a.status));
+        tc::fence_after_sync();
+        ++done;
       }
-      if (rq == 0) *reinterpret_cast<float2 *>(red + 8 * c + 2 * cq) = s;
-    }
-    named_sync(1 + half, 128);
-    if (quarter == 0) {
-      const int h = 32 * half + lane;
-      const float ls = (sm->red[0][h] + sm->red[1][h]) + (sm->red[2][h] + sm->red[3][h]);
-      const float mr = sm->mref[h];
-      if (h < nh) {
-        if (splits > 1) {
-          reinterpret_cast<float2 *>(a.part_ml)[((size_t)it.qq * a.H + it.h0 + h) * splits + split] = make_float2(mr, ls);
-        } else {  // fold in the sink (logit sink[h], value 0) and normalise
-          const float sk = a.sink[it.h0 + h] * kLog2e, M = fmaxf(mr, sk), wm = ex2_approx(mr - M);
-          const float Ls = ls * wm + ex2_approx(sk - M);
-          sm->norm[h] = Ls == 0.f ? 0.f : wm / Ls;
-        }
-      }
-      sm->mref[h] = kFloor;  // for the next item, which reads it after a barrier
-      if (it.ntiles > 0) tc::mbar_arrive(&sm->norm_full);
-    }
-    named_sync(1 + half, 128);
-    // These warps' half of the output (all of it where the item has no tiles).
-    const bool some = it.ntiles > 0;
-    if (some) {
-      ok = __all_sync(0xffffffffu, ok && wait(&sm->o_done, done & 1, abort, a.status));
-      tc::fence_after_sync();
-      ++done;
-    }
-    if (!ok) break;
-    write_out<NB>(a, tmem + 32 * half, sm->norm + 32 * half, (size_t)it.qq * a.H + it.h0 + 32 * half, nh - 32 * half, quarter, 0,
-                  some ? NB / 2 : NB, some, &sm->o_free);
+      if (ok)
+        write_out<NB>(a, tmem + 32 * half, sm->norm[which] + 32 * half, (size_t)it.qq * a.H + it.h0 + 32 * half, nh - 32 * half, quarter, 0,
+                      some ? NB / 2 : NB, some, &sm->o_free);
     }
   }
   tc::fence_before_sync();

@@ -314,3 +314,36 @@ def test_wrappers_refuse_bad_shapes(cuda_device):
             ops.paged_sparse_mqa(**{**args, **kw})
     with pytest.raises(_lib.CsaError):
         ops.paged_sparse_mqa(**{**args, "idx": idx[:, :0]})
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["int4", "rows"])
+@pytest.mark.parametrize("Q,B,H,D,W", [(450, 450, 64, 512, 0), (400, 2, 64, 512, 70), (170, 1, 100, 256, 3), (310, 31, 5, 128, 64)])
+def test_many_queries_of_all_lengths(cuda_device, fmt, Q, B, H, D, W):
+    # more queries than SMs, lists from empty to several tiles in any order, used slots behind unused ones
+    N, k, page = 200, 200, 16
+    c = _inputs(Q + H, Q, B, H, D, N, page, W, fmt, BF16)
+    g = c["g"]
+    idx = torch.full((Q, k), -1, dtype=torch.int32)
+    for i in range(Q):
+        m = int(torch.randint(0, k + 1, (1,), generator=g)) * int(i % 3 > 0)
+        at = torch.randperm(k, generator=g)[:m]  # anywhere in the list
+        idx[i, at] = torch.randperm(N, generator=g)[:m].to(torch.int32)
+    ws = ops.Workspace(cuda_device)
+    for _ in range(2):
+        out = _run(cuda_device, c, W, D ** -0.5, idx=idx, ws=ws)
+        assert ws.status() == 0
+    R.check_attention(out, _refs(c, W, D ** -0.5, idx=idx), BF16, k + W)
+    n_cmp = torch.randint(0, N + 1, (Q,), generator=g, dtype=torch.int32)
+    n_cmp[::5] = 0
+    out = _run(cuda_device, c, W, D ** -0.5, n_cmp=n_cmp, ws=ws)
+    assert ws.status() == 0
+    R.check_attention(out, _refs(c, W, D ** -0.5, n_cmp=n_cmp), BF16, N + W)
+
+
+@gpu
+def test_workspace_on_another_device_is_refused(cuda_device):
+    c = _inputs(1, 2, 2, 4, 32, 8, 4, 3, "int4", BF16)
+    ws = ops.Workspace("cpu")
+    with pytest.raises(ValueError, match="ws is on"):
+        _run(cuda_device, c, 3, 0.1, idx=torch.zeros(2, 3, dtype=torch.int32), ws=ws)
