@@ -83,19 +83,17 @@ __device__ __forceinline__ float group_scale(float amax) {
 // The codes of 8 values. v / s as v (1 / s), off by 2^-23 of it at most, next to
 // the 2^-4 of the rounding to E4M3 that follows: the same code but for quotients
 // within 2^-23 of the middle between two.
-__device__ __forceinline__ uint2 codes8(const uint64_t (&v)[4], float s) {
-  uint32_t c[4];
+__device__ __forceinline__ uint2 codes8(uint64_t (&v)[4], float s) {
+  if (s < 0x1p-120f) {  // 1 / s may overflow: both up by 2^100, exactly
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], pack2(0x1p100f, 0x1p100f));
+    s *= 0x1p100f;
+  }
   const float inv = 1.f / s;
   const uint64_t inv2 = pack2(inv, inv);
+  uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 x = unpack2(mul2(v[i], inv2));
-    if (s < 0x1p-120f) {  // 1 / s may overflow
-      const float2 y = unpack2(v[i]);
-      x = make_float2(y.x / s, y.y / s);
-    }
-    c[i] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-  }
+  for (int i = 0; i < 4; ++i) c[i] = __nv_cvt_float2_to_fp8x2(unpack2(mul2(v[i], inv2)), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
@@ -175,8 +173,9 @@ __global__ void __launch_bounds__(32 * WPR *RPB, 2048 / (32 * WPR * RPB)) add_rm
   if constexpr (kFp8) {
     uint8_t *out = static_cast<uint8_t *>(a.out) + r * a.D;
     const int lanes = a.group / 8;  // lanes that hold a group (a group of 32..256 dims lies in one warp's vectors)
+    const int shift = __ffs(lanes) - 1;  // (a power of two here)
     if (a.group < a.D) {
-      float *scales = a.scales + r * (a.D / a.group);
+      float *scales = a.scales + r * (nvec >> shift);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int j = t + 32 * WPR * i;
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(32 * WPR *RPB, 2048 / (32 * WPR * RPB)) add_rm
         if (live && j < nvec) {
           const float s = group_scale(m);
           *reinterpret_cast<uint2 *>(out + 8 * j) = codes8(v[i], s);
-          if (j % lanes == 0) scales[j / lanes] = s;
+          if ((j & (lanes - 1)) == 0) scales[j >> shift] = s;
         }
       }
     } else {

@@ -74,6 +74,9 @@ __device__ __forceinline__ void store16(T *p, const float (&v)[16], int n, bool 
     if (i < n) p[i] = from_f<T>(v[i]);
 }
 
+// t / G by a product: m = ceil(2^32 / G), exact while t G < 2^32 (0 for G = 1).
+__device__ __forceinline__ int quotient(int t, uint32_t m) { return m ? (int)__umulhi((uint32_t)t, m) : t; }
+
 // Slots of the block's rows [r0, r0 + rb) of sequence b (-1: nothing there).
 __device__ __forceinline__ void block_slots(const PagedRowsArgs &a, int b, int r0, int rb, long long *slot) {
   for (int i = threadIdx.x; i < rb; i += blockDim.x) {
@@ -303,7 +306,8 @@ __device__ __forceinline__ void append_rotated(const PagedRowsArgs &a, int b, in
 // Blocks [0, turn_blocks) take the rows' ends from dim d16 on, turn_rb rows each; the others the dims before, rb rows each.
 template <typename T, bool kInt4>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedRowsArgs a, int rb, int chunks, int turn_rb,
-                                                                int turn_chunks, int turn_blocks, int d16, bool vec) {
+                                                                int turn_chunks, int turn_blocks, int d16, uint32_t per_g,
+                                                                bool vec) {
   __shared__ long long slot[kMaxRows];
   __shared__ Turn turns[kTurns];
   __shared__ alignas(16) T rot[kInt4 ? kRotElems : 1];
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedRowsArgs a,
   const T *rows = static_cast<const T *>(a.rows) + b * a.seq_stride + (long long)r0 * a.row_stride;
   uint8_t *pages = const_cast<uint8_t *>(a.cache.pages);
   for (int t = threadIdx.x; t < rb * G; t += blockDim.x) {
-    const int i = t / G, g = t - i * G, d = 16 * g;
+    const int i = quotient(t, per_g), g = t - i * G, d = 16 * g;
     if (slot[i] < 0) continue;
     if constexpr (kInt4) {
       Group<T> v;
@@ -343,7 +347,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedRowsArgs a,
 }
 
 template <typename T, bool kInt4>
-__global__ void __launch_bounds__(kThreads) paged_read_kernel(PagedRowsArgs a, int rb, int chunks, bool vec) {
+__global__ void __launch_bounds__(kThreads) paged_read_kernel(PagedRowsArgs a, int rb, int chunks, uint32_t per_g,
+                                                              bool vec) {
   __shared__ long long slot[kMaxRows];
   pdl_wait();
   pdl_release();
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(PagedRowsArgs a, i
   const int G = (D + 15) / 16;
   T *out = static_cast<T *>(const_cast<void *>(a.rows)) + b * a.seq_stride + (long long)r0 * a.row_stride;
   for (int t = threadIdx.x; t < rb * G; t += blockDim.x) {
-    const int i = t / G, g = t - i * G, d = 16 * g;
+    const int i = quotient(t, per_g), g = t - i * G, d = 16 * g;
     if (slot[i] < 0) continue;
     float v[16];
     const int n = min(16, D - d);
@@ -418,11 +423,13 @@ cudaError_t launch_rows(const PagedRowsArgs &a, bool append, cudaStream_t stream
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int items = max(rb * ((d16 + 15) / 16), turn_blocks ? turn_rb * ((D - d16) / 2) : 0);
   const int threads = min((items + 31) / 32 * 32, kThreads);
+  const int G = (d16 + 15) / 16;
+  const uint32_t per_g = G > 1 ? (uint32_t)(((1ull << 32) + G - 1) / G) : 0;
   if (append)
     return launch_pdl(int4 ? paged_append_kernel<T, true> : paged_append_kernel<T, false>, dim3((unsigned)blocks),
-                      dim3(threads), 0, stream, a, rb, (int)chunks, turn_rb, (int)turn_chunks, (int)turn_blocks, d16, vec);
+                      dim3(threads), 0, stream, a, rb, (int)chunks, turn_rb, (int)turn_chunks, (int)turn_blocks, d16, per_g, vec);
   return launch_pdl(int4 ? paged_read_kernel<T, true> : paged_read_kernel<T, false>, dim3((unsigned)blocks), dim3(threads), 0,
-                    stream, a, rb, (int)chunks, vec);
+                    stream, a, rb, (int)chunks, per_g, vec);
 }
 
 }  // namespace
