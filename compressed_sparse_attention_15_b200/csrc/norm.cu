@@ -6,9 +6,10 @@
 // of the residual stream that the next layer reads; every sum is fp32.
 //
 // Bytes bound it: x, the residual, h and the output move once each, the row
-// staying in registers between the sum of squares and the output. With 16 bf16
-// values a thread its instructions come close behind (4,096 rows of 4,096 with
-// 8-bit output: 31 us at one instruction a value and step), so they are packed:
+// staying in registers between the sum of squares and the output. Its instructions
+// come close behind (4,096 rows of 4,096 with 8-bit output took 31 us at one
+// instruction a value and step, and takes 23.3 packed: 5.1 TB/s; with bf16 output
+// 21.7: 6.2 TB/s), so they are packed:
 // x + residual as bf16 pairs (a sum of two bf16 numbers rounds the same from its
 // exact value as from its fp32 one, as what fp32 drops is below 2^-16 of it), the
 // rest as fp32 pairs.
@@ -112,8 +113,10 @@ __device__ __forceinline__ float row_reduce(float v, float (&red)[RPB][WPR], int
   return v;
 }
 
-// WPR warps per row, NV vectors of 8 dims per thread (vector t + 32 WPR i),
-// RPB rows per block.
+// WPR warps per row, NV vectors of 8 dims per thread (vector t + 32 WPR i), RPB
+// rows per block. Two vectors a thread at most, for rows in flight: with four (or
+// two rows a block) the 4,096-dim case took 35 to 39 us where it took 31; and all
+// of an SM's threads (32 registers each), 30 us for rows of 16,384 where 37 without.
 template <typename T, int WPR, int NV, int RPB, bool kFp8>
 __global__ void __launch_bounds__(32 * WPR *RPB, 2048 / (32 * WPR * RPB)) add_rmsnorm_kernel(NormArgs a) {
   __shared__ float red[RPB][WPR];

@@ -31,12 +31,22 @@
 // heads of a query) in turn, and each role runs ahead into the next item, so that
 // its loads, its queries' and its first products overlap the end of the last. Row
 // lists differ in length (a selection ends at its last used slot), so a block
-// claims its next item, by a counter in the workspace, while it works on one: with
-// items dealt out in advance the last block of 148 finished a third after the mean.
+// claims its next item, by a counter in the workspace, when the lookups of the one
+// it works on are done.
+//
+// What bounds it. A tile's products take the tensor pipe 1,800 cycles (S^T 32 MMAs
+// of 32, P.V 16 of 48: their operands' shared-memory reads), widening it 4,096
+// words at 13 instructions; it goes by in about 2,800, at half an instruction a
+// cycle and scheduler and the tensor pipe 37 % active, because each tile's way
+// through the five roles is a chain of waits and only two tiles fit. Measured: 16
+// sequences of 8,192 entries 34 us (17.2 GFLOP: 0.30 of the measured tensor peak;
+// the same rows in bf16 would take 21 us to read), 1,024 prefill queries over up to
+// 512 entries each 108 us, 32 decode queries over 512 of 16,383 entries 15 us. Code
+// size counts: 130 KB of it, with every wait and loop in line, ran 1.3 times as long.
 //
 // Roles (640 threads): warps 0-7 widen (or copy bf16 rows), warps 8-15 run the
 // softmax and write the output, warp 16 loads the queries and issues S^T, warp
-// 17 issues P.V and owns TMEM, warps 18 and 19 look rows up and fetch them. All
+// 17 issues P.V and owns TMEM, warps 18 and 19 look rows up. All
 // mbarrier waits are bounded; the softmax warps of a half take every decision to
 // stop together.
 #include "attn.cuh"
@@ -969,8 +979,8 @@ int paged_mqa_tc_splits(int Q, int H, int D, int rows_max) {
   if (D % 128 || D > 512) return 0;
   const int tiles = (rows_max + 2 * kRows - 1) / kRows;  // (the window's padding to whole tiles)
   const long long qv = (long long)Q * ((H + kH - 1) / kH);
-  // a block per SM, and no split below two tiles: a split of one tile writes and has merged as many bytes of
-  // partials as two, for half of the work
+  // a block per SM, and no split below two tiles: its partials are as many bytes to write and to merge for half of
+  // the work (one query's 130 tiles: 16.7 us with one tile at least, 15.6 with two, 17.9 with three)
   long long s = device_sm_count() / qv;
   if (s > tiles / 2) s = tiles / 2;
   return (int)(s < 1 ? 1 : s > kPagedMaxSplits ? kPagedMaxSplits : s);
