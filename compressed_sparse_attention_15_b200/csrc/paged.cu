@@ -277,7 +277,8 @@ __device__ __forceinline__ void append_rotated(const PagedRowsArgs &a, int b, in
       for (int k = 0; k < kAhead; ++k) {
         const int i = i0 + k * at_once;
         if (i >= rb) break;
-        const T y0 = from_f<T>((float)(x[k].x * at.x - x[k].y * at.y)), y1 = from_f<T>((float)(x[k].x * at.y + x[k].y * at.x));
+        T y0 = from_f<T>((float)(x[k].x * at.x - x[k].y * at.y)), y1 = from_f<T>((float)(x[k].x * at.y + x[k].y * at.x));
+        if (j < lead) y0 = from_f<T>(x[k].x), y1 = from_f<T>(x[k].y);  // (a turn by nothing would make inf * 0 of them)
         at = make_double2(at.x * u.step.x - at.y * u.step.y, at.y * u.step.x + at.x * u.step.y);
         if constexpr (kInt4) {
           rot[i * E + 2 * j] = y0;

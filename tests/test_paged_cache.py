@@ -304,3 +304,19 @@ def test_wrappers_refuse_bad_shapes(cuda_device):
         ops.paged_read(pages, scales, table, e0, 3, out=z(2, 4, 32))
     with pytest.raises((ValueError, TypeError)):
         ops.paged_read(pages, scales, table, e0, 3, out=z(2, 3, 64)[:, :, :32])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_infinity_in_front_of_a_rotation_inside_its_group(cuda_device, dtype):
+    # dims 32 .. 39 are not rotated and share their scale with 40 .. 47, which are
+    kv = torch.ones(1, 2, 64, dtype=dtype)
+    kv[0, 0, 33], kv[0, 1, 38] = float("inf"), float("-inf")
+    pages, scales, table = R.make_cache(11, 1, 2, 2, 64, "int4", dtype)
+    e0 = torch.zeros(1, dtype=torch.int32)
+    p, s = _append(cuda_device, kv, pages, scales, table, e0, None, (24, 10000.0, None, 3))
+    got = ops.paged_read(p, s, table.to(cuda_device), e0.to(cuda_device), 2, dtype=F32).cpu()[0]
+    want = torch.zeros(2, 16)
+    want[0, 1], want[1, 6] = 7 * 448, -7 * 448
+    assert torch.equal(got[:, 32:48], want)
+    assert torch.isfinite(got).all()
