@@ -215,11 +215,12 @@ def _call(name: str, dev: int, *args):
 
 
 def _workspace(ws, device, dev: int, nbytes: int = 256):
-    """(pointer, size) of a workspace on device number dev."""
+    """A workspace's buffer on device number dev. The caller holds it until the launch: memory
+    given back before that could be another thread's by then."""
     w = (ws or Workspace(device)).get(nbytes)
     if w.get_device() != dev:
         raise ValueError(f"ws is on {w.device}, expected {device}")
-    return w.data_ptr(), w.numel()
+    return w
 
 
 def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, fp8: bool = False, group: int = 0, out=None,
@@ -531,8 +532,9 @@ def paged_append(kv, pages, scales, page_table, entry0, n_new=None, rope=None, w
     nn = None if n_new is None else _per_sequence(n_new, "n_new", torch.int32, B, dev)
     rope_dims, theta, pos0, pos_stride = rope or (0, 0.0, None, 0)
     pos = None if pos0 is None else _per_sequence(pos0, "pos0", torch.int64, B, dev)
+    w = _workspace(ws, kv.device, dev)
     _call("csa_paged_append", dev, kv.data_ptr(), rs, ss, p, s, t, e0, nn, B, n, D, num_pages, page_size, per, int(rope_dims),
-          float(theta), pos, int(pos_stride), code, cache, *_workspace(ws, kv.device, dev))
+          float(theta), pos, int(pos_stride), code, cache, w.data_ptr(), w.numel())
     return pages
 
 
@@ -565,8 +567,9 @@ def paged_read(pages, scales, page_table, entry0, n: int, n_new=None, out=None, 
             raise ValueError("out's sequences must not overlap")
     e0 = _per_sequence(entry0, "entry0", torch.int32, B, dev)
     nn = None if n_new is None else _per_sequence(n_new, "n_new", torch.int32, B, dev)
+    w = _workspace(ws, pages.device, dev)
     _call("csa_paged_read", dev, p, s, t, e0, nn, out.data_ptr(), ss, B, n, D, num_pages, page_size, per, code, cache,
-          *_workspace(ws, pages.device, dev))
+          w.data_ptr(), w.numel())
     return out
 
 
@@ -603,8 +606,9 @@ def _paged_mqa(name, q, pages, scales, page_table, rows, kv_win, win_end, sink, 
         raise ValueError("out must have q's shape")
     k = (rows.shape[1],) if sparse else ()
     nbytes = _lib.lib().csa_paged_mqa_workspace_bytes(Q, H, D, (k[0] if sparse else per * page_size) + win_len)
+    w = _workspace(ws, q.device, dev, nbytes)
     _call(name, dev, q.data_ptr(), p, s, t, r, win, sk, float(scale), o, Q, B, H, D, num_pages, page_size, per, *k, win_len,
-          end, T_raw, int(q_per_seq), code, cache, *_workspace(ws, q.device, dev, nbytes))
+          end, T_raw, int(q_per_seq), code, cache, w.data_ptr(), w.numel())
     return out
 
 

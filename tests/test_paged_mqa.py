@@ -2,6 +2,7 @@
 values that the cache holds (paged_reference.check_attention has the bound)."""
 import ctypes
 import math
+import weakref
 
 import pytest
 import torch
@@ -347,3 +348,34 @@ def test_workspace_on_another_device_is_refused(cuda_device):
     ws = ops.Workspace("cpu")
     with pytest.raises(ValueError, match="ws is on"):
         _run(cuda_device, c, 3, 0.1, idx=torch.zeros(2, 3, dtype=torch.int32), ws=ws)
+
+
+@gpu
+def test_a_call_s_own_workspace_lives_until_the_launch(cuda_device, monkeypatch):
+    made = []
+
+    class Recorded(ops.Workspace):
+        def get(self, nbytes):
+            w = super().get(nbytes)
+            made.append(weakref.ref(w))
+            return w
+
+    call, names = ops._call, []
+
+    def checked(name, *args):
+        assert made[-1]() is not None, name
+        names.append(name)
+        call(name, *args)
+
+    monkeypatch.setattr(ops, "Workspace", Recorded)
+    monkeypatch.setattr(ops, "_call", checked)
+    Q, H, D, N = 2, 4, 128, 40
+    c = _inputs(41, Q, Q, H, D, N, 16, 0, "int4", BF16)
+    d = {n: (t.to(cuda_device) if isinstance(t, torch.Tensor) else t) for n, t in c.items()}
+    cache, e0 = (d["pages"], d["scales"], d["table"]), torch.zeros(Q, dtype=torch.int32, device=cuda_device)
+    ops.paged_append(d["q"], *cache, e0)
+    ops.paged_read(*cache, e0, 3)
+    ops.paged_hca_mqa(d["q"], *cache, e0, None, None, d["sink"], 0.1, 0)
+    ops.paged_sparse_mqa(d["q"], *cache, e0[:, None].contiguous(), None, None, d["sink"], 0.1, 0)
+    torch.cuda.synchronize()
+    assert len(names) == len(made) == 4
