@@ -45,24 +45,40 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None, contiguous=True):
 
 
 class Workspace:
-    """A reusable device workspace (first 256 bytes: the status word)."""
+    """A reusable device workspace (first 256 bytes: the status word).
+
+    Memory that a captured graph uses stays allocated as long as the workspace:
+    a buffer that captured calls were given is kept when a later call needs a
+    larger one, and one that is first needed inside a capture, where its zeros
+    are written by that graph's replays, serves that call alone."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self._captured = False  # a captured graph uses buf
+        self._of_graphs = []    # buffers that only captured graphs use
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(256, int(nbytes))
+        capturing = self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()
         if self.buf is None or self.buf.numel() < nbytes:
-            # zero-filled: the status word, and the counters of csa_decode_step
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            # zero-filled: the status word, and the counters of csa_decode_step and the paged attention
+            buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            if capturing:
+                self._of_graphs.append(buf)
+                return buf
+            if self._captured:
+                self._of_graphs.append(self.buf)
+            self.buf, self._captured = buf, False
+        self._captured |= capturing
         return self.buf
 
     def status(self) -> int:
         """Synchronise, return and clear the status word (0 = clean)."""
-        if self.buf is None:
-            return 0
-        return workspace_status(self.buf)
+        v = 0 if self.buf is None else workspace_status(self.buf)
+        for buf in self._of_graphs:
+            v |= workspace_status(buf)
+        return v
 
 
 def workspace_status(ws: torch.Tensor) -> int:

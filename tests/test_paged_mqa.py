@@ -379,3 +379,36 @@ def test_a_call_s_own_workspace_lives_until_the_launch(cuda_device, monkeypatch)
     ops.paged_sparse_mqa(d["q"], *cache, e0[:, None].contiguous(), None, None, d["sink"], 0.1, 0)
     torch.cuda.synchronize()
     assert len(names) == len(made) == 4
+
+
+@gpu
+def test_graphs_keep_the_workspace_that_they_were_captured_with(cuda_device):
+    # Q items above the grid's blocks: the counters in the workspace are used
+    Q, H, D, N, W = 170, 64, 128, 70, 0
+    c = _inputs(43, Q, 2, H, D, N, 16, W, "int4", BF16)
+    dev = cuda_device
+    d = {n: (t.to(dev) if isinstance(t, torch.Tensor) else t) for n, t in c.items()}
+    n_cmp = torch.arange(Q, dtype=torch.int32) % (N + 1)
+    args = (d["q"], d["pages"], d["scales"], d["table"], n_cmp.to(dev), None, None, d["sink"], 0.1, W)
+    want = ops.paged_hca_mqa(*args)
+    refs = _refs(c, W, 0.1, n_cmp=n_cmp)
+    R.check_attention(want, refs, BF16, N)
+    for first in (False, True):  # a workspace that is new to a capture; one that an eager call has used
+        ws = ops.Workspace(dev)
+        if first:
+            ops.paged_hca_mqa(*args, ws=ws)
+        graphs, outs = [], []
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                outs.append(ops.paged_hca_mqa(*args, ws=ws))
+            graphs.append(g)
+        ws.get(1 << 20)  # a larger call's
+        other = torch.full((1 << 18,), 255, dtype=torch.uint8, device=dev)  # (into what was given back, if anything was)
+        eager = ops.paged_hca_mqa(*args, ws=ws)
+        for g in (graphs[1], graphs[0], graphs[1]):
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want) and all(torch.equal(o, want) for o in outs)
+        assert torch.all(other == 255)
+        assert ws.status() == 0
