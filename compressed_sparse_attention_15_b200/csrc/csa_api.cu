@@ -163,7 +163,8 @@ int csa_add_rmsnorm(const void *x, long long x_stride, const void *residual, con
   if (!fp8 && (out_dtype != dtype || group != 0)) return CSA_ERR_INVALID;
   if (group != 0 && ((group != 32 && group != 64 && group != 128 && group != 256) || D % group)) return CSA_ERR_INVALID;
   if (rows == 0) return CSA_OK;
-  if (!x || !weight || !out || (residual != nullptr) != (sum_out != nullptr)) return CSA_ERR_INVALID;
+  if (!x || !weight || !out || (residual != nullptr) != (sum_out != nullptr) || sum_out == out)
+    return CSA_ERR_INVALID;
   if (fp8 && (!out_scales || (reinterpret_cast<uintptr_t>(out_scales) & 3))) return CSA_ERR_INVALID;
   if (!elem_aligned(x, dtype) || !elem_aligned(residual, dtype) || !elem_aligned(sum_out, dtype) ||
       (!fp8 && !elem_aligned(out, dtype)) || (reinterpret_cast<uintptr_t>(weight) & 3))
@@ -431,7 +432,7 @@ static int paged_rows(const void *rows, long long row_stride, long long seq_stri
   if (row_stride < D || seq_stride < 0 || (!append && B > 1 && n > 0 && seq_stride < (n - 1) * row_stride + D))
     return CSA_ERR_INVALID;
   if (rope_dims < 0 || rope_dims > D || rope_dims % 8 ||
-      (rope_dims && (D % 2 || !(rope_theta > 1.0) || pos_stride < 0)) || (reinterpret_cast<uintptr_t>(pos0) & 7))
+      (rope_dims && (D % 2 || !(rope_theta > 1.0) || isinf(rope_theta) || pos_stride < 0)) || (reinterpret_cast<uintptr_t>(pos0) & 7))
     return CSA_ERR_INVALID;
   if (!ws || !ws_aligned(ws) || ws_bytes < kStatusBytes) return CSA_ERR_WORKSPACE;
   if (B == 0 || n == 0) return CSA_OK;

@@ -215,7 +215,7 @@ int csa_hadamard_rows(const void *x, void *out, float *out_scales, long long row
  *   x       : [rows, D] dtype, rows x_stride elements apart (0 means D).
  *   residual, sum_out, out : [rows, D], dense. sum_out may be residual or x
  *             (with x_stride D); out may be x or residual (same type); no
- *             other overlap.
+ *             other overlap (sum_out = out is refused).
  *   weight  : [D] float32.
  * Limits: 1 <= D <= 16384, eps >= 0, group 0 or one of 32, 64, 128, 256 that
  * divides D (E4M3 only). rows = 0 does nothing. Returns CSA_ERR_INVALID before
@@ -520,7 +520,7 @@ int csa_decode_step(const csa_decode_step_args *args, void *ws, size_t ws_bytes,
  *   entry0  : [B] int32.   n_new : [B] int32 (0 .. n) or NULL (n everywhere).
  *   pos0    : [B] int64 or NULL (zeros). pos_stride >= 0: tokens per entry.
  *   rope_dims a multiple of 8, <= D (0: none; the rest is then not read);
- *   D even and rope_theta > 1 with it.
+ *   D even and rope_theta > 1 (and finite) with it.
  * csa_paged_read: the inverse: out[b, i] = values of entry entry0[b] + i for
  *   i < n_new[b]; rows from n_new[b] on are left as they were.
  *   out     : [B, n, D] dtype, dense rows, sequences out_seq_stride apart (0:

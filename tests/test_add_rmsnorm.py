@@ -195,3 +195,9 @@ def test_wrapper_refuses_bad_shapes(cuda_device):
         ops.add_rmsnorm(z(2, 64), z(64))
     with pytest.raises(_lib.CsaError):
         ops.add_rmsnorm(z(2, 64), w, eps=-1.0)
+
+
+def test_refuses_one_tensor_for_both_outputs():
+    build()
+    N, P, P2 = ctypes.c_void_p(0), ctypes.c_void_p(4096), ctypes.c_void_p(8192)  # never dereferenced
+    assert _lib.lib().csa_add_rmsnorm(P, 0, P, P, 1e-6, P2, N, P2, 2, 64, 0, 1, 1, N) == 1

@@ -320,3 +320,10 @@ def test_infinity_in_front_of_a_rotation_inside_its_group(cuda_device, dtype):
     want[0, 1], want[1, 6] = 7 * 448, -7 * 448
     assert torch.equal(got[:, 32:48], want)
     assert torch.isfinite(got).all()
+
+
+def test_append_refuses_an_infinite_base():
+    build()
+    N, P = ctypes.c_void_p(0), ctypes.c_void_p(4096)  # P is never dereferenced
+    for theta in (float("inf"), float("nan")):
+        assert _lib.lib().csa_paged_append(P, 0, 0, P, P, P, P, N, 2, 3, 64, 5, 16, 2, 8, theta, N, 1, 1, 3, P, 256, N) == 1
