@@ -44,6 +44,9 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
+_stream_captures = torch._C._cuda_isCurrentStreamCapturing
+
+
 class Workspace:
     """A reusable device workspace (first 256 bytes: the status word).
 
@@ -55,22 +58,23 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self._capturing = _stream_captures if self.device.type == "cuda" else lambda: False
         self._captured = False  # a captured graph uses buf
         self._of_graphs = []    # buffers that only captured graphs use
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(256, int(nbytes))
-        capturing = self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+        capturing = self._captured or self._capturing()
         if self.buf is None or self.buf.numel() < nbytes:
             # zero-filled: the status word, and the counters of csa_decode_step and the paged attention
             buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            if capturing:
+            if self._capturing():
                 self._of_graphs.append(buf)
                 return buf
             if self._captured:
                 self._of_graphs.append(self.buf)
-            self.buf, self._captured = buf, False
-        self._captured |= capturing
+            self.buf, capturing = buf, False
+        self._captured = capturing
         return self.buf
 
     def status(self) -> int:
