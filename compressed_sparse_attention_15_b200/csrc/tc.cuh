@@ -161,10 +161,9 @@ __device__ __forceinline__ void fence_after_sync() {
 }
 
 // True in one lane of a converged warp, always the same one. MMAs issued under
-// a branch on it, by a warp that is converged around that branch, take their
-// descriptors straight from uniform registers; under `lane == 0` every operand
-// is first moved there, at 46 cycles an MMA alone and about 95 beside busy
-// warps, where M = 64, N = 64, K = 16 takes the tensor pipe 32.
+// a branch on it, by a warp that is converged around that branch, go at the
+// tensor pipe's rate (32 cycles for M = 64, N = 64, K = 16); under `lane == 0`
+// each took 46 cycles alone and about 95 beside busy warps.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
