@@ -78,6 +78,9 @@ constexpr float kFloor = -1e30f;  // running maximum of no rows (finite: no inf 
 struct Small {
   // per tile buffer (and half of the dims): filled, read; per tile buffer: S^T made, P^T written
   uint64_t kv_full[2][2], kv_empty[2][2], s_full[2];
+  // The same, of a window tile copied in bulk: its bytes are there. (Barriers of the
+  // issuing thread alone: their phases end with the bytes, whichever role gives up.)
+  uint64_t win_full[2][2];
   uint64_t p_full;                             // P^T written
   uint64_t slot_full[2], slot_empty[2];        // a tile's slots: published, read
   uint64_t pv_done[4];                         // P.V made, per tile (mod 4)
@@ -120,6 +123,9 @@ struct Item {
   int qq, h0, b;
   int nsel, wlo, nwin, w64;
   int t0, ntiles;
+
+  // Tile li holds 64 rows of the window on end, and is copied in bulk.
+  __device__ __forceinline__ bool bulk(int li) const { return (t0 + li + 1) * kRows <= nwin; }
 };
 
 // The waits of this kernel: one try in line, the rest (with its limit) out of
@@ -404,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 2; ++j) {
         tc::mbar_init(&sm->kv_full[i][j], 32 * kLoadWarps);
         tc::mbar_init(&sm->kv_empty[i][j], 1);
+        tc::mbar_init(&sm->win_full[i][j], 1);
       }
       tc::mbar_init(&sm->s_full[i], 1);
     }
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // Half of an item's output is these warps' to write. They do so when both
     // tile buffers hold tiles of the items after it, and have nothing else to do.
-    int tma_last = -1;  // the last tile that this thread had copied in bulk
+    uint32_t bulk_made = 0, bulk_phase = 0;  // bit g: tiles copied in bulk into buffer g: some, the parity of their number
     int out_qv = -1;
     uint32_t out_at = 0, done = 0;  // the tile before which it is written; items written
     auto output = [&] {
@@ -530,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && wait(&sm->kv_empty[g][i], free_phase, abort, a.status);
           ok = __all_sync(0xffffffffu, ok);
           const int r0 = (L.t0 + li) * kRows;
-          if (ok && in_win && r0 + kRows <= L.nwin) {
+          if (ok && L.bulk(li)) {
             // 64 rows of the window on end: bulk copies, which land while the next tile is widened. (Not so where
             // rows of the tile lie outside the window: those must not be read.)
             if (lane < kRowsPerWarp) sm->valid[g][my_row] = 1;
@@ -538,17 +545,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int i = 0; i < kParts; ++i) {
                 const int b0 = 4 * i, b1 = min(NB, b0 + 4);
-                tc::mbar_arrive_expect_tx(&sm->kv_full[g][i], (b1 - b0) * kBoxBytes);
+                tc::mbar_arrive_expect_tx(&sm->win_full[g][i], (b1 - b0) * kBoxBytes);
 #pragma unroll 1
                 for (int bx = b0; bx < b1; ++bx)
                   tc::tma_load_2d(kv + g * kTileBytes + bx * kBoxBytes, &tm_win, 64 * bx, L.b * a.T_raw + L.wlo + r0,
-                                  &sm->kv_full[g][i]);
+                                  &sm->win_full[g][i]);
               }
-              tma_last = T;
-            } else {
-#pragma unroll
-              for (int i = 0; i < kParts; ++i) tc::mbar_arrive(&sm->kv_full[g][i]);
+              bulk_made |= 1u << g;
+              bulk_phase ^= 1u << g;
             }
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) tc::mbar_arrive(&sm->kv_full[g][i]);
           } else if (ok) {
             if (lane < kRowsPerWarp) sm->valid[g][my_row] = slot >= 0;
             const bf16 *base = in_win ? static_cast<const bf16 *>(a.kv_win) + (size_t)L.b * a.T_raw * kD
@@ -578,9 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (out_qv >= 0) output();
     cp_async_wait_all();
-    if (!ok && tma_last >= 0)  // (nothing is in flight when the block ends; without a fault every tile was used)
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) tc::mbar_drain(&sm->kv_full[tma_last & 1][i], (tma_last >> 1) & 1);
+    // Nothing is in flight when the block ends: a buffer's last bulk copy has landed, or is waited for here (the one
+    // before it was used: the buffer was free again).
+    for (int g = 0; g < 2; ++g)
+      if (bulk_made >> g & 1)
+        for (int i = 0; i < kParts; ++i) tc::mbar_drain(&sm->win_full[g][i], ((bulk_phase >> g) & 1) ^ 1);
   } else if (warp >= kFetchWarp0) {
     // ------------------------------------------------------------ lookups
     // A lane looks one row up.
@@ -670,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t ad_kv = tc::sw128_desc(tc::smem_u32(kv), 16, 1024), bd_q = tc::sw128_desc(tc::smem_u32(qs), 16, 1024);
     auto ready = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
     uint32_t T = 0, done = 0;  // tiles and items (with tiles) so far
+    uint32_t bulk_phase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Item it;
@@ -694,12 +704,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < kParts; ++i) {
           if (!(ok = ready(&sm->kv_full[buf][i], (T >> 1) & 1))) break;
+          if (it.bulk(li) && !(ok = ready(&sm->win_full[buf][i], (bulk_phase >> buf) & 1))) break;
           tc::fence_after_sync();
           if (tc::elect_one())
             issue_s<NB>(tmem + kColS + 64 * buf, ad_kv + (uint64_t)((buf * kTileBytes) >> 4), bd_q, i);
           __syncwarp();
         }
         if (!ok) break;
+        if (it.bulk(li)) bulk_phase ^= 1u << buf;
         if (tc::elect_one()) {
           tc::commit(&sm->s_full[buf]);
           if (li == it.ntiles - 1) tc::commit(&sm->q_empty);
@@ -718,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t ad_v = tc::sw128_desc(tc::smem_u32(kv), kBoxBytes, 1024);
     const uint64_t bd_p = tc::sw128_desc(tc::smem_u32(ps), kPBytes, 1024);
     auto ready = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
-    uint32_t T = 0, done = 0;
+    uint32_t T = 0, done = 0, bulk_phase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Item it;
@@ -730,6 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int li = 0; li < ntiles; ++li, ++T) {
         const int buf = T & 1;
         for (int i = 0; i < kParts; ++i) ok = ok && ready(&sm->kv_full[buf][i], (T >> 1) & 1);  // (the tile's writes)
+        if (it.bulk(li)) {
+          for (int i = 0; i < kParts; ++i) ok = ok && ready(&sm->win_full[buf][i], (bulk_phase >> buf) & 1);
+          bulk_phase ^= 1u << buf;
+        }
         if (!ok || !(ok = ready(&sm->p_full, T & 1))) break;
         tc::fence_after_sync();
         if (tc::elect_one()) {

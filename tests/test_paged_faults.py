@@ -32,3 +32,39 @@ def test_wait_timeout_raises_status_and_returns(cuda_device, Q, W):
     out = _run(cuda_device, c, W, D ** -0.5, idx=idx, ws=ws)
     assert ws.status() == 0
     R.check_attention(out, _refs(c, W, D ** -0.5, idx=idx), BF16, 1 + W)
+
+
+@pytest.mark.parametrize("D", [128, 512])
+@pytest.mark.parametrize("Q", [2, 300])
+def test_teardown_with_window_copies_in_flight(cuda_device, Q, D):
+    # Four whole window tiles a query: both tile buffers may be filling in bulk when the wait for one of them runs out.
+    # The block waits for their bytes, not for the roles that left, so the call returns at once (a copy takes
+    # microseconds; waiting for a phase that nobody completes would take the 2 s of the drain's own limit).
+    H, N, W = 64, 90, 300
+    c = _inputs(Q + D, Q, Q, H, D, N, 64, W, "int4", BF16)
+    c["win_end"][:] = c["kv_win"].shape[1] - 1
+    n_cmp = torch.arange(Q, dtype=torch.int32) % (N + 1)
+    d = {n: (t.to(cuda_device) if isinstance(t, torch.Tensor) else t) for n, t in c.items()}
+    ws = ops.Workspace(cuda_device)
+
+    def call():
+        return ops.paged_hca_mqa(d["q"], d["pages"], d["scales"], d["table"], n_cmp.to(cuda_device), d["kv_win"], d["win_end"],
+                                 d["sink"], D ** -0.5, W, ws=ws)
+
+    call()
+    assert ws.status() == 0
+    limit = ws.buf[8:16].view(torch.int64)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    for ns in (1, 2000, 1, 4000):
+        limit.fill_(ns)
+        start.record()
+        call()
+        end.record()
+        torch.cuda.synchronize()
+        assert start.elapsed_time(end) < 1000, "the block waited for a phase that nobody completes"
+        assert ws.status() in (0, 8)
+        assert torch.all(ws.buf[16:256] == 0), "the counters are back at zero"
+    limit.zero_()
+    out = call()
+    assert ws.status() == 0
+    R.check_attention(out, _refs(c, W, D ** -0.5, n_cmp=n_cmp), BF16, N + W)
