@@ -201,3 +201,38 @@ def test_refuses_one_tensor_for_both_outputs():
     build()
     N, P, P2 = ctypes.c_void_p(0), ctypes.c_void_p(4096), ctypes.c_void_p(8192)  # never dereferenced
     assert _lib.lib().csa_add_rmsnorm(P, 0, P, P, 1e-6, P2, N, P2, 2, 64, 0, 1, 1, N) == 1
+
+
+def _nearest_e4m3(q):
+    """The E4M3 value nearest to q (64 bits), ties to the even one."""
+    step = torch.ldexp(torch.ones_like(q), torch.frexp(q)[1].clamp(min=-5) - 4)
+    return torch.round(q / step) * step
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("group", [0, 32, 256])
+def test_codes_at_and_next_to_ties_are_the_quotient_s(cuda_device, dtype, group):
+    # Rows of +-1 without eps have a norm of 1: y is +- the weight, any fp32 number. Every group's scale s has 18
+    # bits, its largest weight is 448 s, the others are the middles between two E4M3 values times s (exact), or one
+    # fp32 step beside them: quotients that are ties, or at least 2^-24 of themselves away from one.
+    D = 4096
+    g = torch.Generator().manual_seed(group)
+    n = group or D
+    s = torch.randint(1 << 17, 1 << 18, (D // n, 1), generator=g).double() * 2.0 ** torch.randint(-40, 20, (D // n, 1), generator=g)
+    t = torch.randint(16, 32, (D // n, n), generator=g).double() * 2.0 ** torch.randint(-10, 4, (D // n, n), generator=g)
+    low = torch.randint(0, 16, (D // n, n), generator=g).double() * 2.0 ** -10  # among the subnormals, and zero
+    w = (s * torch.where(torch.rand(D // n, n, generator=g) < 0.2, low, t)).float()
+    w = torch.nextafter(w, w * torch.randint(0, 3, w.shape, generator=g))  # one step down, none or up
+    w[:, 0] = (448 * s[:, 0]).float()
+    sign = torch.randint(0, 2, (3, D), generator=g) * 2 - 1
+    quotient = (w.double() / s).float()  # the fp32 quotient (53 bits are enough for its rounding to be that of y / s)
+    want = _nearest_e4m3(quotient.double().flatten() * sign).clamp(-448, 448)
+    x = sign.to(dtype).to(cuda_device)
+    buf = torch.zeros(3 * D + 16, dtype=torch.uint8, device=cuda_device)
+    for out in (buf[:3 * D].view(3, D), buf[3:3 + 3 * D].view(3, D)):  # 8-byte aligned, and not
+        codes, scales = ops.add_rmsnorm(x, w.flatten().to(cuda_device), eps=0.0, fp8=True, group=group, out=out)
+        assert torch.equal(scales.cpu().double(), s.T.expand(3, -1))
+        got = codes.view(torch.float8_e4m3fn).cpu().double()
+        assert torch.equal(got, want), f"{int((got != want).sum())} of {want.numel()} codes"
+        assert torch.equal(codes.cpu() >> 7 != 0, sign < 0), "the sign stays, of zeros too"
