@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t ad_v = tc::sw128_desc(tc::smem_u32(kv), kBoxBytes, 1024);
     const uint64_t bd_p = tc::sw128_desc(tc::smem_u32(ps), kPBytes, 1024);
     auto ready = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, a.status); };
-    uint32_t T = 0, done = 0, bulk_phase = 0;
+    uint32_t T = 0, done = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Item it;
@@ -741,11 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (done > 0 && !(ok = ready(&sm->o_free, (done - 1) & 1))) break;
       for (int li = 0; li < ntiles; ++li, ++T) {
         const int buf = T & 1;
-        for (int i = 0; i < kParts; ++i) ok = ok && ready(&sm->kv_full[buf][i], (T >> 1) & 1);  // (the tile's writes)
-        if (it.bulk(li)) {
-          for (int i = 0; i < kParts; ++i) ok = ok && ready(&sm->win_full[buf][i], (bulk_phase >> buf) & 1);
-          bulk_phase ^= 1u << buf;
-        }
+        for (int i = 0; i < kParts; ++i) ok = ok && ready(&sm->kv_full[buf][i], (T >> 1) & 1);  // (the tile's writes; of
+        // one copied in bulk S^T has waited for the bytes and read them, and P^T comes after S^T)
         if (!ok || !(ok = ready(&sm->p_full, T & 1))) break;
         tc::fence_after_sync();
         if (tc::elect_one()) {
