@@ -8,6 +8,7 @@ arithmetic of the method. Names follow the C entry points.
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -44,45 +45,108 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-_stream_captures = torch._C._cuda_isCurrentStreamCapturing
+_RELAXED = 2              # cudaStreamCaptureModeRelaxed
+_captured = []            # (mark of a live graph, the workspace buffer that it uses)
+_captured_lock = threading.Lock()
+_zeroing = {}             # device number -> the stream that zeroes buffers while another is captured
+
+
+def _drop_ended():
+    """Lets go of the buffers whose graphs are gone."""
+    with _captured_lock:
+        if _captured:
+            ended = _lib.lib().csa_graph_mark_ended
+            _captured[:] = [c for c in _captured if not ended(c[0])]
+
+
+def _zeros_beside_capture(nbytes: int, device) -> torch.Tensor:
+    """Zeros, at once and in ordinary memory, while the current stream is captured."""
+    mode = ctypes.c_int(_RELAXED)
+    _lib.check("csa_exchange_capture_mode", _lib.lib().csa_exchange_capture_mode(ctypes.byref(mode)))
+    try:
+        side = _zeroing.get(device.index)
+        if side is None:
+            side = _zeroing[device.index] = torch.cuda.Stream(device)
+        with torch.cuda.stream(side):
+            buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        side.synchronize()
+    finally:
+        _lib.check("csa_exchange_capture_mode", _lib.lib().csa_exchange_capture_mode(ctypes.byref(mode)))
+    return buf
 
 
 class Workspace:
     """A reusable device workspace (first 256 bytes: the status word).
 
-    Memory that a captured graph uses stays allocated as long as the workspace:
-    a buffer that captured calls were given is kept when a later call needs a
-    larger one, and one that is first needed inside a capture, where its zeros
-    are written by that graph's replays, serves that call alone."""
+    Eager and captured calls share one buffer, which grows where a call needs
+    more. A graph keeps what its calls were given: a buffer lives on, at its
+    address, until the last graph captured with it is gone, also when a larger
+    one has taken its place or the workspace is dropped. Buffers are zeroed
+    when they are made, never by a graph, so status bits stay until they are
+    read. (A workspace for_one_call, which none but its call knows, is a
+    captured graph's own memory, zeroed by the graph.)"""
 
-    def __init__(self, device=None):
+    _side = False      # buf was made beside a capture
+    _captures = ()     # captures that buf has been marked in
+    _older = ()        # buffers that graphs still use, replaced since
+
+    def __init__(self, device=None, for_one_call: bool = False):
         self.device = torch.device(device or "cuda")
         self.buf = None
-        self._capturing = _stream_captures if self.device.type == "cuda" else lambda: False
-        self._captured = False  # a captured graph uses buf
-        self._of_graphs = []    # buffers that only captured graphs use
+        self._for_one_call = for_one_call
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(256, int(nbytes))
-        capturing = self._captured or self._capturing()
-        if self.buf is None or self.buf.numel() < nbytes:
-            # zero-filled: the status word, and the counters of csa_decode_step and the paged attention
-            buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            if self._capturing():
-                self._of_graphs.append(buf)
-                return buf
-            if self._captured:
-                self._of_graphs.append(self.buf)
-            self.buf, capturing = buf, False
-        self._captured = capturing
+        small = self.buf is None or self.buf.numel() < nbytes
+        if self.device.type != "cuda" or not _capturing(self.device):
+            if small:
+                # zero-filled: the status word, and the counters of csa_decode_step and the paged attention
+                self._take(torch.zeros(nbytes, dtype=torch.uint8, device=self.device))
+            elif self._side:  # (used on a stream that it does not belong to)
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
+            return self.buf
+        if self._for_one_call:
+            return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        device = torch.device("cuda", torch.cuda.current_device()) if self.device.index is None else self.device
+        if small:
+            self._take(_zeros_beside_capture(nbytes, device))
+            self._side = True
+        self._mark(device)
         return self.buf
+
+    def _take(self, buf):
+        if self._captures:
+            self._older, self._captures = (*self._older, self.buf), ()
+        self.buf, self._side = buf, False
+
+    def _mark(self, device):
+        L, number, mark = _lib.lib(), ctypes.c_ulonglong(0), ctypes.c_void_p()
+        stream = _stream(device)
+        _lib.check("csa_graph_mark", L.csa_graph_mark(stream, ctypes.byref(number), None))
+        if number.value not in self._captures:
+            _drop_ended()
+            _lib.check("csa_graph_mark", L.csa_graph_mark(stream, ctypes.byref(number), ctypes.byref(mark)))
+            with _captured_lock:
+                _captured.append((mark, self.buf))
+            self._captures = (*self._captures, number.value)
 
     def status(self) -> int:
         """Synchronise, return and clear the status word (0 = clean)."""
         v = 0 if self.buf is None else workspace_status(self.buf)
-        for buf in self._of_graphs:
+        for buf in self._older:
             v |= workspace_status(buf)
+        _drop_ended()
+        with _captured_lock:
+            self._older = tuple(b for b in self._older if any(c[1] is b for c in _captured))
         return v
+
+
+def _capturing(device) -> bool:
+    """Whether the current stream of a device is being captured into a graph."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def workspace_status(ws: torch.Tensor) -> int:
@@ -237,7 +301,7 @@ def _call(name: str, dev: int, *args):
 def _workspace(ws, device, dev: int, nbytes: int = 256):
     """A workspace's buffer on device number dev. The caller holds it until the launch: memory
     given back before that could be another thread's by then."""
-    w = (ws or Workspace(device)).get(nbytes)
+    w = (ws or Workspace(device, for_one_call=True)).get(nbytes)
     if w.get_device() != dev:
         raise ValueError(f"ws is on {w.device}, expected {device}")
     return w
@@ -324,7 +388,7 @@ def index_topk(qi, wi, ki, n_cmp, k: int, q_per_seq=None, out=None, ws: Workspac
     _need(out, "out", dtype=torch.int32, device=qi.device)
     L = _lib.lib()
     nbytes = L.csa_index_topk_workspace_bytes(Q, N_max, k)
-    w = (ws or Workspace(qi.device)).get(nbytes)
+    w = (ws or Workspace(qi.device, for_one_call=True)).get(nbytes)
     rc = L.csa_index_topk(_ptr(qi), _ptr(wi), _ptr(ki), _ptr(n_cmp), int(k), _ptr(out), Q, B, Hi, Di, N_max, qps,
                           _dtype_code(qi), _ptr(w), w.numel(), _stream(qi.device))
     _lib.check("csa_index_topk", rc)
@@ -338,7 +402,7 @@ def index_scores(qi, wi, ki, n_cmp, q_per_seq=None, out=None, ws: Workspace | No
     if out is None:
         out = torch.full((Q, N_max), float("nan"), dtype=torch.float32, device=qi.device)
     _need(out, "out", dtype=torch.float32, device=qi.device)
-    w = (ws or Workspace(qi.device)).get(256)
+    w = (ws or Workspace(qi.device, for_one_call=True)).get(256)
     rc = _lib.lib().csa_index_scores(_ptr(qi), _ptr(wi), _ptr(ki), _ptr(n_cmp), _ptr(out), Q, B, Hi, Di, N_max,
                                      qps, _dtype_code(qi), _ptr(w), w.numel(), _stream(qi.device))
     _lib.check("csa_index_scores", rc)
@@ -354,7 +418,7 @@ def topk(scores, n_cmp, k: int, out=None, ws: Workspace | None = None):
         out = torch.empty((Q, k), dtype=torch.int32, device=scores.device)
     _need(out, "out", dtype=torch.int32, device=scores.device)
     L = _lib.lib()
-    w = (ws or Workspace(scores.device)).get(L.csa_topk_workspace_bytes(Q, N_max, k))
+    w = (ws or Workspace(scores.device, for_one_call=True)).get(L.csa_topk_workspace_bytes(Q, N_max, k))
     rc = L.csa_topk(_ptr(scores), _ptr(n_cmp), int(k), _ptr(out), Q, N_max, _ptr(w), w.numel(),
                     _stream(scores.device))
     _lib.check("csa_topk", rc)
@@ -388,7 +452,7 @@ def index_scores_fp8(qi8, sq, wi, ki8, sk, n_cmp, q_per_seq=None, out=None, ws: 
     if out is None:
         out = torch.full((Q, N_max), float("nan"), dtype=torch.float32, device=qi8.device)
     _need(out, "out", dtype=torch.float32, device=qi8.device)
-    w = (ws or Workspace(qi8.device)).get(256)
+    w = (ws or Workspace(qi8.device, for_one_call=True)).get(256)
     rc = _lib.lib().csa_index_scores_fp8(_ptr(qi8), _ptr(sq), _ptr(wi), _ptr(ki8), _ptr(sk), _ptr(n_cmp), _ptr(out),
                                          Q, B, Hi, Di, N_max, qps, _ptr(w), w.numel(), _stream(qi8.device))
     _lib.check("csa_index_scores_fp8", rc)
@@ -402,7 +466,7 @@ def index_topk_fp8(qi8, sq, wi, ki8, sk, n_cmp, k: int, q_per_seq=None, out=None
         out = torch.empty((Q, k), dtype=torch.int32, device=qi8.device)
     _need(out, "out", dtype=torch.int32, device=qi8.device)
     L = _lib.lib()
-    w = (ws or Workspace(qi8.device)).get(L.csa_index_topk_workspace_bytes(Q, N_max, k))
+    w = (ws or Workspace(qi8.device, for_one_call=True)).get(L.csa_index_topk_workspace_bytes(Q, N_max, k))
     rc = L.csa_index_topk_fp8(_ptr(qi8), _ptr(sq), _ptr(wi), _ptr(ki8), _ptr(sk), _ptr(n_cmp), int(k), _ptr(out),
                               Q, B, Hi, Di, N_max, qps, _ptr(w), w.numel(), _stream(qi8.device))
     _lib.check("csa_index_topk_fp8", rc)
@@ -441,7 +505,7 @@ def sparse_mqa(q, kv_cmp, idx, kv_win, win_end, sink, scale: float, win_len: int
         out = torch.empty_like(q)
     _need(out, "out", dtype=q.dtype, device=q.device)
     L = _lib.lib()
-    w = (ws or Workspace(q.device)).get(L.csa_mqa_workspace_bytes(Q, H, D, k + win_len))
+    w = (ws or Workspace(q.device, for_one_call=True)).get(L.csa_mqa_workspace_bytes(Q, H, D, k + win_len))
     rc = L.csa_sparse_mqa(_ptr(q), _ptr(kv_cmp), _ptr(idx), _ptr(kv_win), _ptr(sink), float(scale), _ptr(out), Q, B,
                           H, D, N_max, k, int(win_len), _ptr(win_end), T_raw, qps, _dtype_code(q), _ptr(w),
                           w.numel(), _stream(q.device))
@@ -466,7 +530,8 @@ def topk_sparse_mqa(scores, n_cmp, k: int, q, kv_cmp, kv_win, win_end, sink, sca
     _need(out, "out", dtype=q.dtype, device=q.device)
     _need(idx_out, "idx_out", dtype=torch.int32, device=q.device)
     L = _lib.lib()
-    w = (ws or Workspace(q.device)).get(L.csa_topk_sparse_mqa_workspace_bytes(Q, H, D, N_max, int(k), int(win_len)))
+    w = (ws or Workspace(q.device, for_one_call=True)).get(
+        L.csa_topk_sparse_mqa_workspace_bytes(Q, H, D, N_max, int(k), int(win_len)))
     rc = L.csa_topk_sparse_mqa(_ptr(scores), _ptr(n_cmp), int(k), _ptr(idx_out), _ptr(q), _ptr(kv_cmp), _ptr(kv_win),
                                _ptr(sink), float(scale), _ptr(out), Q, B, H, D, N_max, int(win_len), _ptr(win_end),
                                T_raw, qps, _dtype_code(q), _ptr(w), w.numel(), _stream(q.device))
@@ -483,7 +548,7 @@ def hca_mqa(q, kv_cmp, n_cmp, kv_win, win_end, sink, scale: float, win_len: int,
         out = torch.empty_like(q)
     _need(out, "out", dtype=q.dtype, device=q.device)
     L = _lib.lib()
-    w = (ws or Workspace(q.device)).get(L.csa_mqa_workspace_bytes(Q, H, D, N_max + win_len))
+    w = (ws or Workspace(q.device, for_one_call=True)).get(L.csa_mqa_workspace_bytes(Q, H, D, N_max + win_len))
     rc = L.hca_mqa(_ptr(q), _ptr(kv_cmp), _ptr(kv_win), _ptr(sink), float(scale), _ptr(out), Q, B, H, D, N_max,
                    _ptr(n_cmp), int(win_len), _ptr(win_end), T_raw, qps, _dtype_code(q), _ptr(w), w.numel(),
                    _stream(q.device))
@@ -721,7 +786,7 @@ def decode_step(q, kv_cmp, kv_win, win_end, sink, scale: float, win_len: int, n_
                 a.pos0 = _ptr(pos0)
             a.rope_dims, a.rope_theta = int(rope_dims), float(theta)
     L = _lib.lib()
-    w = (ws or Workspace(q.device)).get(L.csa_decode_step_workspace_bytes(ctypes.byref(a)))
+    w = (ws or Workspace(q.device, for_one_call=True)).get(L.csa_decode_step_workspace_bytes(ctypes.byref(a)))
     rc = L.csa_decode_step(ctypes.byref(a), _ptr(w), w.numel(), _stream(q.device))
     _lib.check("csa_decode_step", rc)
     return out
