@@ -14,6 +14,11 @@ import torch
 
 from . import _lib
 
+# Torch's own short forms of these calls, without the checks around them; a torch without CUDA has not got them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream_captures = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
 _DT = {torch.float32: _lib.CSA_DTYPE_F32, torch.bfloat16: _lib.CSA_DTYPE_BF16}
 
 
@@ -93,12 +98,14 @@ class Workspace:
     def __init__(self, device=None, for_one_call: bool = False):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self._host = self.device.type != "cuda"
+        self._index = self.device.index
         self._for_one_call = for_one_call
 
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(256, int(nbytes))
         small = self.buf is None or self.buf.numel() < nbytes
-        if self.device.type != "cuda" or not _capturing(self.device):
+        if self._host or not _capturing(self._index):
             if small:
                 # zero-filled: the status word, and the counters of csa_decode_step and the paged attention
                 self._take(torch.zeros(nbytes, dtype=torch.uint8, device=self.device))
@@ -107,7 +114,7 @@ class Workspace:
             return self.buf
         if self._for_one_call:
             return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        device = torch.device("cuda", torch.cuda.current_device()) if self.device.index is None else self.device
+        device = torch.device("cuda", _current_device()) if self._index is None else self.device
         if small:
             self._take(_zeros_beside_capture(nbytes, device))
             self._side = True
@@ -141,12 +148,12 @@ class Workspace:
         return v
 
 
-def _capturing(device) -> bool:
-    """Whether the current stream of a device is being captured into a graph."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.device(device):
-        return torch.cuda.is_current_stream_capturing()
+def _capturing(index) -> bool:
+    """Whether the current stream of device number index (None: of the current device) is being captured into a graph."""
+    if index is None or index == _current_device():
+        return _stream_captures()
+    with torch.cuda.device(index):
+        return _stream_captures()
 
 
 def workspace_status(ws: torch.Tensor) -> int:
@@ -272,10 +279,6 @@ def hadamard_rows(x, fp8: bool = False):
 # ------------------------------------------------------- norm of the activations
 # The calls from here on are short next to a Python call: their checks take one
 # look at each tensor, and pointers go to the library as plain integers.
-
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-
 
 def _check(t, name: str, dtype, dev: int, contiguous: bool = True):
     """_need for a tensor of a dtype on CUDA device number dev."""

@@ -1,10 +1,17 @@
 """The Python binding marshals arguments only: every entry point refuses host
 (CPU) tensors with an error instead of computing anything itself, so there is
 no CPU fallback behind the C ABI. Runs without a GPU."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from compressed_sparse_attention_15_b200 import ops
+from compressed_sparse_attention_15_b200.build import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 f32, bf16, i32, u8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
@@ -37,3 +44,20 @@ CALLS = {
 def test_host_tensors_are_refused(name):
     with pytest.raises(ValueError, match="CUDA tensor"):
         CALLS[name]()
+
+
+def test_imports_on_a_torch_without_cuda():
+    # such a build has none of torch._C's _cuda_* functions; the host functions work there
+    code = """
+import torch
+for name in dir(torch._C):
+    if name.startswith("_cuda_"):
+        delattr(torch._C, name)
+import compressed_sparse_attention_15_b200 as csa
+assert csa.num_entries(64, 8, 4) == 15
+print(csa.ops.visible_entries(torch.tensor([7, 63]), 8, 4).tolist(), csa.synth.__name__, csa.workloads.__name__)
+"""
+    build()
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.startswith("[1, 15] ")
