@@ -502,8 +502,11 @@ int csa_decode_step(const csa_decode_step_args *args, void *ws, size_t ws_bytes,
  *                (lowest first) and dims 1, 3, 5, 7 in those of its high half.
  *   scales     : [num_pages, page_size, D / 16] E4M3 (4 bits), else NULL.
  *   page_table : [B, pages_per_seq] int32 device array. A page may stand in
- *                several tables (a shared prefix); what two rows of one
- *                append write to the same place is either's.
+ *                several tables (a shared prefix). Rows of one append that go
+ *                to the same place leave a mixture there: every element is one
+ *                of the rows', and in 4 bits every 16 dims' codes are one's
+ *                and their scale is one's, not always the same one's, so that
+ *                the values can be neither's. Other rows are not affected.
  *   page_size  : any size >= 1.
  * pages_per_seq * page_size is the capacity of a sequence (up to 2^31 - 2^20
  * entries). Offsets are 64-bit. A code page is 8-byte aligned and D a multiple

@@ -327,3 +327,37 @@ def test_append_refuses_an_infinite_base():
     N, P = ctypes.c_void_p(0), ctypes.c_void_p(4096)  # P is never dereferenced
     for theta in (float("inf"), float("nan")):
         assert _lib.lib().csa_paged_append(P, 0, 0, P, P, P, P, N, 2, 3, 64, 5, 16, 2, 8, theta, N, 1, 1, 3, P, 256, N) == 1
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["int4", "rows"])
+@pytest.mark.parametrize("rope", [None, (24, 10000.0, None, 1)])
+def test_rows_of_one_append_at_the_same_place(cuda_device, fmt, rope):
+    # Sequences 0 and 1 share their first page, and write to it with scales 1,000 apart: what is left there is a
+    # mixture of the two; their other pages hold their own rows.
+    D, page, n = 64, 8, 16
+    g = torch.Generator().manual_seed(12)
+    kv = torch.randn(2, n, D, generator=g)
+    kv[1] *= 1000
+    kv = kv.to(BF16)
+    pages, scales, table = R.make_cache(12, 2, n, page, D, fmt, BF16)
+    apart = _append(cuda_device, kv, pages, scales, table, torch.zeros(2, dtype=torch.int32), None, rope)
+    shared = table.clone()
+    shared[1, 0] = shared[0, 0]
+    got = _append(cuda_device, kv, pages, scales, shared, torch.zeros(2, dtype=torch.int32), None, rope)
+    rows = [[None if t is None else t.cpu().view(torch.uint8 if fmt == "int4" else torch.int16)[table[b, 0].long()] for t in apart]
+            for b in range(2)]
+    there = [None if t is None else t.cpu().view(torch.uint8 if fmt == "int4" else torch.int16)[table[0, 0].long()] for t in got]
+    if fmt == "int4":  # 8 bytes of codes at a time
+        one, two, left = (t[0].view(torch.int64) for t in (*rows, there))
+        assert torch.all((there[1] == rows[0][1]) | (there[1] == rows[1][1]))
+    else:
+        one, two, left = (t[0] for t in (*rows, there))
+    assert torch.all((left == one) | (left == two))
+    for a, b, before in zip(apart, got, (pages, scales)):
+        if a is not None:
+            a, b, before = (t.cpu().view(torch.uint8) for t in (a, b, before))
+            for i in (0, 1):
+                assert torch.equal(a[table[i, 1]], b[table[i, 1]])
+            untouched = [p for p in range(len(a)) if p not in table[:, 1].tolist() + [int(table[0, 0])]]
+            assert torch.equal(b[untouched], before[untouched])
