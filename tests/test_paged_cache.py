@@ -361,3 +361,45 @@ def test_rows_of_one_append_at_the_same_place(cuda_device, fmt, rope):
                 assert torch.equal(a[table[i, 1]], b[table[i, 1]])
             untouched = [p for p in range(len(a)) if p not in table[:, 1].tolist() + [int(table[0, 0])]]
             assert torch.equal(b[untouched], before[untouched])
+
+
+def _nearest_e4m3(q):
+    """The E4M3 value nearest to q (64 bits), ties to the even one, at most 448."""
+    step = torch.ldexp(torch.ones_like(q), torch.frexp(q)[1].clamp(min=-5) - 4)
+    return (torch.round(q / step) * step).clamp(max=448)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("unaligned", [False, True])
+@pytest.mark.parametrize("D,rope_dims", [(64, 0), (64, 24), (512, 64), (320, 8), (1024, 1024), (4096, 264)])
+def test_scales_are_those_of_the_stored_values(cuda_device, D, rope_dims, dtype, unaligned):
+    # Every group has a size of its own (1,000 between the largest and the smallest), so that a maximum over another
+    # group, or over values before they are rotated, is far off. The rotated values' rounding and recurrence move a
+    # group's maximum by a factor within 1 +- u, the fp32 division by 1 +- 2^-24, and E4M3 keeps order: the stored
+    # scale lies between the E4M3 values nearest to the two ends, and is the one nearest where nothing is rotated.
+    B, n, page = 2, 40, 16
+    g = torch.Generator().manual_seed(D + rope_dims)
+    size = torch.exp(torch.rand(B, n, D // 16, 1, generator=g) * 6.9 - 3.45)
+    kv = (torch.randn(B, n, D // 16, 16, generator=g) * size).reshape(B, n, D).to(dtype)
+    pages, scales, table = R.make_cache(13, B, n, page, D, "int4", dtype)
+    rope = (rope_dims, 160000.0, torch.tensor([17, 70000]), 4) if rope_dims else None
+    moved = torch.cat([torch.zeros(1, dtype=dtype), kv.flatten()]).to(cuda_device)[1:].view(B, n, D)
+    given = moved if unaligned else kv.to(cuda_device)
+    assert bool(given.data_ptr() % 16) == unaligned
+    on = [t.to(cuda_device) for t in (pages, scales, table, torch.zeros(B, dtype=torch.int32))]
+    ops.paged_append(given, *on, rope=rope and (*rope[:2], rope[2].to(cuda_device), rope[3]))
+    want = R.rotated(kv, rope, rope[2]) if rope else kv.double()
+    got = R.e4m3(on[1].cpu().view(torch.uint8))
+    u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+    for b in range(B):
+        e = torch.arange(n)
+        s = got[table[b].long()[e // page], e % page]
+        amax = want[b].reshape(n, D // 16, 16).abs().amax(-1)
+        turned = torch.arange(D // 16) >= (D - rope_dims) // 16
+        # the rotation's own error, of the pair's length (at most 1.5 times the larger of its two): see the top
+        off = torch.where(turned, u * (1 + 2.0 ** -20) + 2.0 ** -30, 0.0) + 2.0 ** -24
+        lo, hi = _nearest_e4m3(amax / 7 * (1 - off)), _nearest_e4m3(amax / 7 * (1 + off))
+        assert torch.all((lo <= s) & (s <= hi))
+        if dtype == BF16:
+            assert torch.equal(s[:, ~turned], _nearest_e4m3(amax / 7)[:, ~turned])
