@@ -412,3 +412,58 @@ def test_graphs_keep_the_workspace_that_they_were_captured_with(cuda_device):
         assert torch.equal(eager, want) and all(torch.equal(o, want) for o in outs)
         assert torch.all(other == 255)
         assert ws.status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("fmt,dtype", [("int4", BF16), ("rows", BF16), ("int4", F32)])
+@pytest.mark.parametrize("H,D", [(64, 512), (128, 128), (5, 64)])
+def test_a_table_far_longer_than_the_visible_list(cuda_device, H, D, fmt, dtype):
+    # a server's table: room for 262,144 entries, pages assigned to the first 100; most splits of the list are empty
+    N, W, page = 100, 70, 64
+    c = _inputs(51 + H, 2, 2, H, D, N, page, W, fmt, dtype)
+    table = torch.full((2, 4096), -1, dtype=torch.int32)
+    table[:, :c["table"].shape[1]] = c["table"]
+    c["table"] = table
+    ws = ops.Workspace(cuda_device)
+    for n_cmp in ([N, 3], [0, N], [0, 0]):
+        n_cmp = torch.tensor(n_cmp, dtype=torch.int32)
+        for rows in (dict(c, q=c["q"][:1], table=table[:1], kv_win=c["kv_win"][:1], win_end=c["win_end"][:1]), c):
+            Q = rows["q"].shape[0]
+            out = _run(cuda_device, rows, W, D ** -0.5, n_cmp=n_cmp[:Q], ws=ws)
+            assert ws.status() == 0
+            R.check_attention(out, _refs(rows, W, D ** -0.5, n_cmp=n_cmp[:Q]), dtype, N + W)
+    out = _run(cuda_device, dict(c, kv_win=None, win_end=None), 0, D ** -0.5, n_cmp=torch.zeros(2, dtype=torch.int32), ws=ws)
+    assert torch.all(out == 0) and ws.status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("which", ["q", "pages", "scales", "kv_win", "out"])
+@pytest.mark.parametrize("fmt", ["int4", "rows"])
+def test_a_tensor_off_the_16_byte_grid(cuda_device, fmt, which):
+    if which == "scales" and fmt == "rows":
+        pytest.skip("no scales")
+    Q, H, D, N, W = 3, 64, 512, 200, 40
+    c = _inputs(61, Q, Q, H, D, N, 16, W, fmt, BF16)
+    n_cmp = torch.tensor([N, 0, 77], dtype=torch.int32)
+    off = 8 if which == "pages" and fmt == "int4" else 2  # bytes (code pages are 8-byte aligned)
+
+    def moved(t):
+        t = t.to(cuda_device)
+        buf = torch.zeros(t.numel() * t.element_size() + 64, dtype=torch.uint8, device=cuda_device)
+        buf = buf[off:off + t.numel() * t.element_size()]
+        view = buf.view(torch.uint8 if t.dtype == torch.float8_e4m3fn else t.dtype).view(t.shape)
+        view.copy_(t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t)
+        assert view.data_ptr() % 16
+        return view
+
+    d = {n: t.to(cuda_device) if isinstance(t, torch.Tensor) else t for n, t in c.items()}
+    out = torch.empty_like(d["q"])
+    if which == "out":
+        out = moved(out)
+    else:
+        d[which] = moved(c[which])
+    ws = ops.Workspace(cuda_device)
+    got = ops.paged_hca_mqa(d["q"], d["pages"], d["scales"], d["table"], n_cmp.to(cuda_device), d["kv_win"], d["win_end"], d["sink"],
+                            D ** -0.5, W, out=out, ws=ws)
+    assert got.data_ptr() == out.data_ptr() and ws.status() == 0
+    R.check_attention(got, _refs(c, W, D ** -0.5, n_cmp=n_cmp), BF16, N + W)
