@@ -56,9 +56,8 @@ SIGNATURES = {
     "csa_paged_hca_mqa": (_I, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _I, _I, _I, _P,
                                _SZ, _P]),
     "csa_workspace_status": (_I, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
-    "csa_graph_mark": (_I, [_P, ctypes.POINTER(ctypes.c_ulonglong), ctypes.POINTER(_P)]),
-    "csa_graph_mark_ended": (_I, [_P]),
     "csa_exchange_capture_mode": (_I, [ctypes.POINTER(_I)]),
+    "csa_stream_create": (_I, [ctypes.POINTER(_P)]),
     "csa_launch_count": (ctypes.c_ulonglong, []),
     "csa_index_topk_noalloc": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "csa_num_entries": (_LL, [_LL, _I, _I]),

@@ -6,8 +6,6 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <new>
-
 #include "common.cuh"
 #include "kernels.h"
 
@@ -570,45 +568,19 @@ int csa_workspace_status(void *ws, csa_stream_t stream, uint32_t *status) {
   return v ? CSA_ERR_DEVICE : CSA_OK;
 }
 
-static void CUDART_CB end_mark(void *mark) { __atomic_store_n(static_cast<int *>(mark), 1, __ATOMIC_RELEASE); }
-
-int csa_graph_mark(csa_stream_t stream, unsigned long long *capture_id, void **mark) {
-  if (!capture_id) return CSA_ERR_INVALID;
-  cudaStreamCaptureStatus status;
-  cudaGraph_t graph = nullptr;
-  cudaError_t e = cudaStreamGetCaptureInfo((cudaStream_t)stream, &status, capture_id, &graph);
-  if (e != cudaSuccess) return cuda_rc(e);
-  if (status != cudaStreamCaptureStatusActive) return CSA_ERR_INVALID;
-  if (!mark) return CSA_OK;
-  int *m = new (std::nothrow) int(0);
-  if (!m) return CSA_ERR_CUDA;
-  cudaUserObject_t object;
-  e = cudaUserObjectCreate(&object, m, end_mark, 1, cudaUserObjectNoDestructorSync);
-  if (e != cudaSuccess) {
-    delete m;
-    return cuda_rc(e);
-  }
-  e = cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove);
-  if (e != cudaSuccess) {
-    cudaUserObjectRelease(object, 1);  // (the mark ends, and stays allocated: nobody can ask for it)
-    return cuda_rc(e);
-  }
-  *mark = m;
-  return CSA_OK;
-}
-
-int csa_graph_mark_ended(void *mark) {
-  int *m = static_cast<int *>(mark);
-  if (!m || !__atomic_load_n(m, __ATOMIC_ACQUIRE)) return 0;
-  delete m;
-  return 1;
-}
-
 int csa_exchange_capture_mode(int *mode) {
   if (!mode || *mode < 0 || *mode > 2) return CSA_ERR_INVALID;
   cudaStreamCaptureMode m = static_cast<cudaStreamCaptureMode>(*mode);
   const cudaError_t e = cudaThreadExchangeStreamCaptureMode(&m);
   *mode = (int)m;
+  return cuda_rc(e);
+}
+
+int csa_stream_create(csa_stream_t *stream) {
+  if (!stream) return CSA_ERR_INVALID;
+  cudaStream_t s = nullptr;
+  const cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  *stream = (csa_stream_t)s;
   return cuda_rc(e);
 }
 

@@ -8,7 +8,6 @@ arithmetic of the method. Names follow the C entry points.
 from __future__ import annotations
 
 import ctypes
-import threading
 
 import torch
 
@@ -50,50 +49,21 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-_RELAXED = 2              # cudaStreamCaptureModeRelaxed
-_captured = []            # (mark of a live graph, the workspace buffer that it uses)
-_captured_lock = threading.Lock()
-_zeroing = {}             # device number -> the stream that zeroes buffers while another is captured
-
-
-def _drop_ended():
-    """Lets go of the buffers whose graphs are gone."""
-    with _captured_lock:
-        if _captured:
-            ended = _lib.lib().csa_graph_mark_ended
-            _captured[:] = [c for c in _captured if not ended(c[0])]
-
-
-def _zeros_beside_capture(nbytes: int, device) -> torch.Tensor:
-    """Zeros, at once and in ordinary memory, while the current stream is captured."""
-    mode = ctypes.c_int(_RELAXED)
-    _lib.check("csa_exchange_capture_mode", _lib.lib().csa_exchange_capture_mode(ctypes.byref(mode)))
-    try:
-        side = _zeroing.get(device.index)
-        if side is None:
-            side = _zeroing[device.index] = torch.cuda.Stream(device)
-        with torch.cuda.stream(side):
-            buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        side.synchronize()
-    finally:
-        _lib.check("csa_exchange_capture_mode", _lib.lib().csa_exchange_capture_mode(ctypes.byref(mode)))
-    return buf
-
-
 class Workspace:
     """A reusable device workspace (first 256 bytes: the status word).
 
     Eager and captured calls share one buffer, which grows where a call needs
-    more. A graph keeps what its calls were given: a buffer lives on, at its
-    address, until the last graph captured with it is gone, also when a larger
-    one has taken its place or the workspace is dropped. Buffers are zeroed
-    when they are made, never by a graph, so status bits stay until they are
-    read. (A workspace for_one_call, which none but its call knows, is a
-    captured graph's own memory, zeroed by the graph.)"""
+    more. It is zeroed when it is made, never by a graph, so status bits stay
+    until they are read. A captured graph uses the buffer at its address: keep
+    the workspace as long as the graph. Buffers that graphs were captured with
+    stay when a larger one takes their place. (One that is first needed inside a
+    capture is the graph's memory, which also lives as long as the graph. So is
+    that of a workspace for_one_call, which none but its call knows; its zeros
+    are the graph's.)"""
 
-    _side = False      # buf was made beside a capture
-    _captures = ()     # captures that buf has been marked in
-    _older = ()        # buffers that graphs still use, replaced since
+    _captured = False  # a graph was captured with buf
+    _older = ()        # buffers that graphs were captured with, replaced since
+    _own_stream = None
 
     def __init__(self, device=None, for_one_call: bool = False):
         self.device = torch.device(device or "cuda")
@@ -105,46 +75,61 @@ class Workspace:
     def get(self, nbytes: int) -> torch.Tensor:
         nbytes = max(256, int(nbytes))
         small = self.buf is None or self.buf.numel() < nbytes
-        if self._host or not _capturing(self._index):
-            if small:
-                # zero-filled: the status word, and the counters of csa_decode_step and the paged attention
-                self._take(torch.zeros(nbytes, dtype=torch.uint8, device=self.device))
-            elif self._side:  # (used on a stream that it does not belong to)
-                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
-            return self.buf
-        if self._for_one_call:
-            return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        device = torch.device("cuda", _current_device()) if self._index is None else self.device
+        capturing = not self._host and _capturing(self._index)
         if small:
-            self._take(_zeros_beside_capture(nbytes, device))
-            self._side = True
-        self._mark(device)
+            if capturing and not self._for_one_call:
+                self._take(self._beside_capture(self._size(nbytes)))
+            else:
+                # zero-filled: the status word, and the counters of csa_decode_step and the paged attention
+                self._take(torch.zeros(self._size(nbytes), dtype=torch.uint8, device=self.device))
+        if capturing:
+            self._captured = True
         return self.buf
 
-    def _take(self, buf):
-        if self._captures:
-            self._older, self._captures = (*self._older, self.buf), ()
-        self.buf, self._side = buf, False
+    def _size(self, nbytes):
+        # where the old buffer stays, half as much again at least: all that stay are less than twice the present one
+        return max(nbytes, self.buf.numel() * 3 // 2) if self._captured else nbytes
 
-    def _mark(self, device):
-        L, number, mark = _lib.lib(), ctypes.c_ulonglong(0), ctypes.c_void_p()
-        stream = _stream(device)
-        _lib.check("csa_graph_mark", L.csa_graph_mark(stream, ctypes.byref(number), None))
-        if number.value not in self._captures:
-            _drop_ended()
-            _lib.check("csa_graph_mark", L.csa_graph_mark(stream, ctypes.byref(number), ctypes.byref(mark)))
-            with _captured_lock:
-                _captured.append((mark, self.buf))
-            self._captures = (*self._captures, number.value)
+    def _take(self, buf):
+        if self._captured:
+            self._older, self._captured = (*self._older, self.buf), False
+        self.buf = buf
+
+    def _beside_capture(self, nbytes: int) -> torch.Tensor:
+        """Memory of the graph that is being captured, zeroed at once, outside the graph.
+
+        The graph's memory pool hands a block that a captured call has given back to a later one on the same
+        stream, and replays write to both. A stream of this workspace's own, forked off the captured one and joined
+        again without any work, has no blocks but this workspace's, so that nothing else ever writes to them. (The
+        stream is never destroyed: another might get its handle, and with it the blocks.)"""
+        device = torch.device("cuda", _current_device() if self._index is None else self._index)
+        mode = ctypes.c_int(2)  # cudaStreamCaptureModeRelaxed: this thread may wait for a stream
+        L = _lib.lib()
+        _lib.check("csa_exchange_capture_mode", L.csa_exchange_capture_mode(ctypes.byref(mode)))
+        try:
+            with torch.cuda.device(device):
+                if self._own_stream is None:
+                    stream = ctypes.c_void_p()
+                    _lib.check("csa_stream_create", L.csa_stream_create(ctypes.byref(stream)))
+                    self._own_stream = torch.cuda.ExternalStream(stream.value, device=device)
+                captured, zeroing = torch.cuda.current_stream(), torch.cuda.Stream()
+                self._own_stream.wait_stream(captured)
+                with torch.cuda.stream(self._own_stream):
+                    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                captured.wait_stream(self._own_stream)
+                with torch.cuda.stream(zeroing):
+                    buf.zero_()
+                zeroing.synchronize()
+        finally:
+            _lib.check("csa_exchange_capture_mode", L.csa_exchange_capture_mode(ctypes.byref(mode)))
+        return buf
 
     def status(self) -> int:
         """Synchronise, return and clear the status word (0 = clean)."""
-        v = 0 if self.buf is None else workspace_status(self.buf)
-        for buf in self._older:
-            v |= workspace_status(buf)
-        _drop_ended()
-        with _captured_lock:
-            self._older = tuple(b for b in self._older if any(c[1] is b for c in _captured))
+        v = 0
+        for buf in (*self._older, self.buf):
+            if buf is not None:
+                v |= workspace_status(buf)
         return v
 
 

@@ -588,22 +588,16 @@ const char *csa_cuda_error_string(int code);
  * CSA_ERR_CUDA if the copy failed. Test/debug use. */
 int csa_workspace_status(void *ws, csa_stream_t stream, uint32_t *status);
 
-/* Workspaces and CUDA graphs: a captured call's workspace has to live as long
- * as the graph, and has to be zero before the graph first runs. These help a
- * caller that manages both (host only; no device memory, nothing launched).
- *
- * csa_graph_mark: while `stream` is being captured, *capture_id takes the
- * number of that capture. With `mark`, *mark takes a mark that is alive as long
- * as the captured graph, or anything instantiated from it, exists or runs.
- * csa_graph_mark_ended: 1 once the mark's graphs are gone (the mark is then
- * freed: ask no more), 0 before.
+/* Two CUDA runtime calls for callers that manage workspaces while a stream is
+ * captured into a graph and have no runtime of their own (host only; nothing
+ * is launched).
  * csa_exchange_capture_mode: sets this thread's cudaStreamCaptureMode to *mode
  * (0 global, 1 thread-local, 2 relaxed) and returns the old one in it: under 2 a
  * thread may allocate and synchronise other streams while it captures one.
- * CSA_ERR_INVALID: a null pointer, or `stream` is not being captured. */
-int csa_graph_mark(csa_stream_t stream, unsigned long long *capture_id, void **mark);
-int csa_graph_mark_ended(void *mark);
+ * csa_stream_create: a non-blocking stream of the current device, the caller's.
+ * Both return CSA_ERR_INVALID for a null pointer or an unknown mode. */
 int csa_exchange_capture_mode(int *mode);
+int csa_stream_create(csa_stream_t *stream);
 
 #ifdef __cplusplus
 }
