@@ -49,6 +49,16 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
+_zeroing = {}  # device number -> the stream that zeroes buffers while another is captured
+
+
+def _new_stream(device):
+    """A stream that nobody else has (torch.cuda.Stream() hands out 32 in turn: one of them may be the captured one)."""
+    stream = ctypes.c_void_p()
+    _lib.check("csa_stream_create", _lib.lib().csa_stream_create(ctypes.byref(stream)))
+    return torch.cuda.ExternalStream(stream.value, device=device)
+
+
 class Workspace:
     """A reusable device workspace (first 256 bytes: the status word).
 
@@ -109,10 +119,10 @@ class Workspace:
         try:
             with torch.cuda.device(device):
                 if self._own_stream is None:
-                    stream = ctypes.c_void_p()
-                    _lib.check("csa_stream_create", L.csa_stream_create(ctypes.byref(stream)))
-                    self._own_stream = torch.cuda.ExternalStream(stream.value, device=device)
-                captured, zeroing = torch.cuda.current_stream(), torch.cuda.Stream()
+                    self._own_stream = _new_stream(device)
+                if device.index not in _zeroing:
+                    _zeroing[device.index] = _new_stream(device)
+                captured, zeroing = torch.cuda.current_stream(), _zeroing[device.index]
                 self._own_stream.wait_stream(captured)
                 with torch.cuda.stream(self._own_stream):
                     buf = torch.empty(nbytes, dtype=torch.uint8, device=device)

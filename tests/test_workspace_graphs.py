@@ -146,6 +146,24 @@ def test_capturing_again_keeps_no_further_buffers(cuda_device):
 
 
 @gpu
+def test_new_workspaces_in_captures_on_every_stream(cuda_device):
+    # torch hands out 32 streams in turn, for captures too
+    scores, n = _inputs(cuda_device, Q=2)
+    want = ops.topk(scores, n, K)
+    kept = []
+    for i in range(70):
+        ws = ops.Workspace(cuda_device)
+        stream = torch.cuda.Stream() if i % 2 else None
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = ops.topk(scores, n, K, ws=ws)
+        kept.append((ws, graph, out))
+    for ws, graph, out in kept:
+        graph.replay()
+        assert torch.equal(out, want) and ws.status() == 0
+
+
+@gpu
 def test_nothing_else_writes_to_a_buffer_made_in_a_capture(cuda_device):
     # blocks that the capture has given back before, of every size and of another workspace, are not taken for it
     scores, n = _inputs(cuda_device, Q=160, seed=7)
