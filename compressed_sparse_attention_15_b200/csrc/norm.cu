@@ -8,8 +8,8 @@
 // Bytes bound it: x, the residual, h and the output move once each, the row
 // staying in registers between the sum of squares and the output. Its instructions
 // come close behind (4,096 rows of 4,096 with 8-bit output took 31 us at one
-// instruction a value and step, and takes 23.3 packed: 5.1 TB/s; with bf16 output
-// 21.7: 6.2 TB/s), so they are packed:
+// instruction a value and step, and takes 23.2 packed: 5.1 TB/s; with bf16 output
+// 21.8: 6.2 TB/s), so they are packed:
 // x + residual as bf16 pairs (a sum of two bf16 numbers rounds the same from its
 // exact value as from its fp32 one, as what fp32 drops is below 2^-16 of it), the
 // rest as fp32 pairs.

@@ -35,13 +35,14 @@
 // it works on are done.
 //
 // What bounds it. A tile's products take the tensor pipe 1,800 cycles (S^T 32 MMAs
-// of 32, P.V 16 of 48: their operands' shared-memory reads), widening it 4,096
-// words at 13 instructions; it goes by in about 2,800, at half an instruction a
-// cycle and scheduler and the tensor pipe 37 % active, because each tile's way
-// through the five roles is a chain of waits and only two tiles fit. Measured: 16
-// sequences of 8,192 entries 34 us (17.2 GFLOP: 0.30 of the measured tensor peak;
-// the same rows in bf16 would take 21 us to read), 1,024 prefill queries over up to
-// 512 entries each 108 us, 32 decode queries over 512 of 16,383 entries 15 us. Code
+// of 32, P.V 16 of 48: their operands' shared-memory reads; with an N of 128 or more
+// the same products would be about 1,030), widening it 4,096 words at 13
+// instructions; it goes by in about 2,800, at half an instruction a cycle and
+// scheduler and the tensor pipe 36 % active, because each tile's way through the five
+// roles is a chain of waits and only two tiles fit. Measured: 16 sequences of 8,192
+// entries 38 us with the merge of 4 (17.2 GFLOP: 0.27 of the measured tensor peak;
+// the same rows in bf16 take 46), 1,024 prefill queries over up to 512 entries each
+// 109 us, 32 decode queries over 512 of 16,383 entries 20 us with the merge. Code
 // size counts: 130 KB of it, with every wait and loop in line, ran 1.3 times as long.
 //
 // Roles (640 threads): warps 0-7 widen (or copy bf16 rows), warps 8-15 run the
@@ -873,9 +874,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        // P = 2^y, rounded to bf16 and summed per head. The sums take the same
-        // bf16 weights as P.V, so that a dominant row's weight (up to 2^8 between
-        // rescales) cancels exactly.
+        // P = 2^y, rounded to bf16 (P.V takes both operands in one type, and V's is
+        // bf16; a second product for what the rounding drops would add 768 cycles to
+        // a tile's 1,800) and summed per head in fp32. The sums take the same bf16
+        // weights as P.V, so that a dominant row's weight (up to 2^8 between rescales)
+        // cancels exactly. A weight is off by 2^-9 of it at most, independently of the
+        // others: next to the output's own rounding (1.7e-3 of its size, r.m.s.) outputs
+        // are off by 1.7e-3 (8,192 rows) to 2.2e-3 (a few rows) in all.
         uint32_t pA[4], pB[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

@@ -20,7 +20,10 @@
  *    is 16-byte aligned take the tensor-core / vectorised kernels; everything
  *    else takes the generic kernels (same results within rounding).
  *  - All arithmetic is fp32 (inputs widened from bf16, products accumulated in
- *    fp32); outputs are rounded once to `dtype` (round to nearest even).
+ *    fp32); outputs are rounded once to `dtype` (round to nearest even). But
+ *    attention on the tensor cores rounds a row's softmax weight to bf16 for its
+ *    product with the row (the sums take the rounded weights too), and forms
+ *    exponentials to about 2^-22.
  *  - Every argument is checked on the host before any launch. A failed check
  *    returns a non-zero code and launches nothing.
  *  - Values that live in device memory (visible counts, indices, window ends)
