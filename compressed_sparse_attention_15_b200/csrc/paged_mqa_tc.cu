@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bf16; a second product for what the rounding drops would add 768 cycles to
         // a tile's 1,800) and summed per head in fp32. The sums take the same bf16
         // weights as P.V, so that a dominant row's weight (up to 2^8 between rescales)
-        // cancels exactly. A weight is off by 2^-9 of it at most, independently of the
+        // cancels exactly. A weight is off by 2^-8 of it at most, independently of the
         // others: next to the output's own rounding (1.7e-3 of its size, r.m.s.) outputs
         // are off by 1.7e-3 (8,192 rows) to 2.2e-3 (a few rows) in all.
         uint32_t pA[4], pB[4];
